@@ -4,16 +4,19 @@
 // it).
 //
 // A tile is TT consecutive tokens of one sequence (aligned to TT), a segment
-// all visible tiles of one sequence for one cached head and one block of 16 of
-// the query heads that share it.  Segments are laid end to end in the order
-// (sequence, cached head, row block), and the line of all tiles is cut into
-// `warps` pieces whose sizes differ by at most one tile: every warp reads the
-// same number of bytes whatever the lengths are.  A segment that a cut falls
-// into is summed in parts:
+// all visible tiles of one sequence for one cached head and one block of the
+// query heads that share it.  A segment costs its tiles and kSegmentUnits
+// tiles' worth beside them (its queries, its result): so many units.  Segments
+// are laid end to end in the order (sequence, cached head, block), and the line
+// of all units is cut into `warps` pieces whose sizes differ by at most one
+// unit.  A warp takes the tiles whose first unit lies in its piece: tile 0 of a
+// segment is at the segment's first unit, tile j at unit kSegmentUnits + j.
+// A segment that a cut falls into is summed in parts:
 //   - the part that begins with the segment lies in the tail slot 2w+1 of its
 //     warp w,
 //   - the part of each later warp w' lies in that warp's head slot 2w'.
-// So a segment's parts are slots 2w+1, 2(w+1), ..., 2*last.
+// So a segment's parts are slots 2w+1, 2(w+1), ..., 2*last (no warp between
+// them is without a tile, since pieces have more than kSegmentUnits units).
 #pragma once
 #include <stdint.h>
 
@@ -25,6 +28,21 @@
 
 namespace fwpkm {
 
+// Division by a fixed page size as a product and a shift: exact for 0 <= t < 2^31
+// (mul is the first integer from 2^shift / d up, 2^31 <= 2^(shift - log2 d) <= 2^32).
+struct PageDiv {
+  uint32_t mul;
+  int shift;
+};
+inline PageDiv page_div(int d) {
+  int s = 0;
+  while ((1ll << s) < d) ++s;
+  const uint64_t top = 1ull << (31 + s);
+  return {(uint32_t)((top + d - 1) / d), 31 + s};
+}
+FWPKM_HD int page_of(PageDiv p, int t) {
+  return (int)(((uint64_t)(uint32_t)t * p.mul) >> p.shift);
+}
 // A sequence's length within what a row of the table can hold; `bad` where it
 // is not the given one.
 FWPKM_HD int cache_length(int len, int width, int page_size, bool &bad) {
@@ -60,16 +78,43 @@ FWPKM_HD Span cache_span(int len, int window, int tile) {
   return s;
 }
 
-// Warps that share `total` tiles: all of them once each has `least` tiles.
-FWPKM_HD int cache_warps(int64_t total, int most, int least) {
-  const int64_t w = total / least;
-  return w < 1 ? 1 : w < most ? (int)w : most;
+constexpr int kSegmentUnits = 2;
+constexpr int kLeastUnits = kSegmentUnits + 2;  // smaller pieces are not worth a warp
+
+FWPKM_HD int64_t segment_units(int tiles) { return (int64_t)tiles + kSegmentUnits; }
+// Unit of tile j, and the first tile at or after unit u of the segment (which
+// may be its number of tiles: none).
+FWPKM_HD int64_t tile_unit(int j) { return j == 0 ? 0 : (int64_t)j + kSegmentUnits; }
+FWPKM_HD int tile_from(int64_t u) {
+  return u == 0 ? 0 : u <= kSegmentUnits ? 1 : (int)(u - kSegmentUnits);
 }
-// First tile of warp w's piece (w == warps: the end of the line).
-FWPKM_HD int64_t cache_cut(int64_t total, int warps, int w) { return total * w / warps; }
-// The warp whose piece holds the tile before `end`.
-FWPKM_HD int cache_last_warp(int64_t total, int warps, int64_t end) {
-  return (int)((end * warps + total - 1) / total) - 1;
+// The line of `total` units cut into `warps` pieces: `more` of q + 1 units,
+// then the others of q.
+struct Line {
+  int64_t total, q;
+  int warps, more;
+};
+FWPKM_HD Line cache_line(int64_t total, int most) {
+  const int64_t w = total / kLeastUnits;
+  Line l;
+  l.total = total;
+  l.warps = w < 1 ? 1 : w < most ? (int)w : most;
+  l.q = total / l.warps;
+  l.more = (int)(total - l.q * l.warps);
+  return l;
+}
+// First unit of warp w's piece (w == warps: the end of the line).
+FWPKM_HD int64_t line_cut(const Line &l, int w) { return l.q * w + (w < l.more ? w : l.more); }
+// The warp whose piece holds a unit.
+FWPKM_HD int line_owner(const Line &l, int64_t unit) {
+  const int64_t big = (l.q + 1) * l.more;
+  return unit < big ? (int)(unit / (l.q + 1)) : l.more + (int)((unit - big) / l.q);
+}
+// Warps of a CTA that take pieces: few pieces are spread over the CTAs, but not
+// thinner than four to a CTA, whose sums join in shared memory.
+FWPKM_HD int line_per_cta(const Line &l, int ctas) {
+  const int n = (l.warps + ctas - 1) / ctas;
+  return n < 4 ? 4 : n;
 }
 
 }  // namespace fwpkm

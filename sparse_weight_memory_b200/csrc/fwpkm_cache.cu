@@ -171,28 +171,36 @@ extern "C" fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache,
   return FWPKM_OK;
 }
 
-// The warps a multiprocessor runs at each width, as in the launches of
-// kernels_cache_attend_*.cu.
-fwpkm::AttendShape fwpkm::attend_shape(int cache_dtype, int dim) {
+// More warps hide more latency; they have to fit the registers (outputs and
+// queries of a segment's heads) and the shared memory (three units each).
+fwpkm::AttendShape fwpkm::attend_shape(int cache_dtype, int dim, int group) {
   const int dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-  int warps = 8;
-  if (cache_dtype == FWPKM_BF16 && dp == 256) warps = 4;
-  if (cache_dtype == FWPKM_F32 && dp >= 128) warps = 4;
-  return {kAttendCtas * warps, dp};
+  if (cache_dtype == FWPKM_F32) {
+    const int heads = group <= 4 ? 4 : 8;
+    return {dp == 64 ? 16 : dp == 128 ? 12 : 8, heads, heads * dp};
+  }
+  const int heads = group <= 8 || dp == 256 ? 8 : 16;
+  int warps = 16;
+  if (dp == 128 && heads == 16) warps = 12;
+  if (dp == 256) warps = cache_dtype == FWPKM_BF16 ? 8 : 12;
+  return {warps, heads, heads * dp};
 }
 
 namespace {
 
-// The workspace: parts, their (maximum, sum), the tails.
+// The workspace: parts, their (m, l), the tails and middles.
 struct Workspace {
-  int64_t ml, tails, bytes;
+  int64_t ml, tails, middles, per, bytes;
 };
-Workspace layout(int cache_dtype, int dim) {
-  const AttendShape s = attend_shape(cache_dtype, dim);
+Workspace layout(int cache_dtype, int dim, int group) {
+  const AttendShape s = attend_shape(cache_dtype, dim, group);
+  const int64_t warps = (int64_t)kAttendCtas * s.warps;
   Workspace w;
-  w.ml = 2ll * s.warps * kAttendRows * s.dp * (int64_t)sizeof(float);
-  w.tails = w.ml + 2ll * s.warps * kAttendRows * (int64_t)sizeof(float2);
-  w.bytes = w.tails + s.warps * (int64_t)sizeof(int4);
+  w.ml = 2 * warps * s.part * (int64_t)sizeof(float);
+  w.tails = w.ml + 2 * warps * s.heads * (int64_t)sizeof(float2);
+  w.middles = w.tails + warps * (int64_t)sizeof(int4);
+  w.per = w.middles + kAttendCtas * (int64_t)sizeof(int4);
+  w.bytes = w.per + kAttendCtas * (int64_t)sizeof(int);
   return w;
 }
 
@@ -212,7 +220,7 @@ extern "C" int64_t fwpkm_cache_attend_workspace(const fwpkm_cache *cache, int B,
   const char *who = "cache_attend_workspace";
   fwpkm_status rc = check_kind(who, cache);
   if (rc == FWPKM_OK) rc = check_heads(who, cache, B, heads);
-  return rc ? (int64_t)rc : layout(cache->dtype, cache->dim).bytes;
+  return rc ? (int64_t)rc : layout(cache->dtype, cache->dim, heads / cache->kv_heads).bytes;
 }
 
 extern "C" fwpkm_status fwpkm_cache_attend(const fwpkm_cache *cache,
@@ -238,7 +246,7 @@ extern "C" fwpkm_status fwpkm_cache_attend(const fwpkm_cache *cache,
     return fail(FWPKM_EINVAL, "%s: out must be given and 16-byte aligned", who);
   if (!std::isfinite(scale)) return fail(FWPKM_EINVAL, "%s: scale must be finite", who);
   if (window < 0) return fail(FWPKM_EINVAL, "%s: window must be >= 0", who);
-  const Workspace w = layout(cache->dtype, cache->dim);
+  const Workspace w = layout(cache->dtype, cache->dim, heads / cache->kv_heads);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < w.bytes)
     return fail(FWPKM_EINVAL, "%s: workspace must be 256-byte aligned and hold %lld bytes", who,
                 (long long)w.bytes);
@@ -250,12 +258,14 @@ extern "C" fwpkm_status fwpkm_cache_attend(const fwpkm_cache *cache,
   a.parts = reinterpret_cast<float *>(ws);
   a.ml = reinterpret_cast<float2 *>(ws + w.ml);
   a.tails = reinterpret_cast<int4 *>(ws + w.tails);
+  a.middles = reinterpret_cast<int4 *>(ws + w.middles);
+  a.per = reinterpret_cast<int *>(ws + w.per);
   a.errors = device_errors;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.heads = heads;
   a.group = heads / a.p.kv_heads;
-  a.blocks = (a.group + kAttendRows - 1) / kAttendRows;
   a.window = window;
+  a.div = page_div(a.p.page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->dtype == FWPKM_F32    ? launch_cache_attend_f32(a, st)
                         : cache->dtype == FWPKM_BF16 ? launch_cache_attend_bf16(a, st)

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/fwpkm_cache.h"
+#include "cache_schedule.cuh"
 #include "fwpkm_internal.cuh"
 
 namespace fwpkm {
@@ -38,11 +39,17 @@ struct AppendArgs {
 cudaError_t launch_cache_append(const AppendArgs &a, int in_dtype, int cache_dtype,
                                 cudaStream_t st);
 
-// Query rows of a segment: the rows of a tensor-core tile.
-constexpr int kAttendRows = 16;
 // Pieces are sized for the B200's 148 multiprocessors (a launch geometry: any
 // other count would only be slower).
 constexpr int kAttendCtas = 148;
+
+// The variant for a cache type, head width and number of query heads to a
+// cached head: warps of a CTA, query heads of a segment, floats of a part.
+// launch_cache_attend_* take the same ones.
+struct AttendShape {
+  int warps, heads, part;
+};
+AttendShape attend_shape(int cache_dtype, int dim, int group);
 
 struct AttendArgs {
   CachePool p;
@@ -51,21 +58,18 @@ struct AttendArgs {
   int64_t q_stride;  // bytes
   char *out;
   float *lse;
-  float *parts;    // [2 * warps][kAttendRows][DP] unnormalised sums of the segments' parts
-  float2 *ml;      // [2 * warps][kAttendRows] their (maximum, sum) in base 2
-  int4 *tails;     // [warps] (sequence, head * blocks + block, last warp) of the segment whose
-                   // first part is the warp's tail slot; last warp -1: none
+  float *parts;  // [2 * warps][part] sums o of the segments' parts
+  float2 *ml;    // [2 * warps][heads] their (m, l)
+  int4 *tails;   // [warps] (sequence, head * blocks + block, last warp) of the segment whose
+                 // first part is the warp's tail slot; last warp -1: none
+  int4 *middles; // [CTAs] (.., last warp, first warp) of the one its first warp is inside of
+  int *per;      // [CTAs] pieces of a CTA, the same for all
   unsigned *errors;
   float scale_log2;  // scale * log2(e)
-  int heads, group, blocks;  // group: query heads of a cached head, in `blocks` blocks of 16 rows
+  int heads, group, blocks;  // group: query heads of a cached head, in `blocks` segments
   int window;
+  PageDiv div;  // by the page size
 };
-// Warps of the launch and the padded head width, by cache type and dim: the
-// layout of the workspace.
-struct AttendShape {
-  int warps, dp;
-};
-AttendShape attend_shape(int cache_dtype, int dim);
 cudaError_t launch_cache_attend_bf16(const AttendArgs &a, cudaStream_t st);
 cudaError_t launch_cache_attend_e4m3(const AttendArgs &a, cudaStream_t st);
 cudaError_t launch_cache_attend_f32(const AttendArgs &a, cudaStream_t st);

@@ -1,26 +1,30 @@
 // kernels_cache_attend.cuh -- attention of one token of each sequence over a
-// paged cache.  Per query row, over the visible tokens t in tiles:
-//   m' = max(m, s_t),  l' = l 2^(m-m') + sum 2^(s_t-m'),
-//   o' = o 2^(m-m') + sum 2^(s_t-m') v_t,      s_t = scale log2(e) q.k_t,
-// and at the end out = o / l, lse = ln 2 (m + log2 l): one pass over the cache.
+// paged cache.  Per query head, over the visible tokens t in tiles:
+//   o = sum 2^(c s_t - m) v_t,   l = sum 2^(c s_t - m),   s_t = q.k_t,
+// c = scale log2(e); where a tile brings a score well above the reference m, o
+// and l are first scaled to a new one.  At the end out = o / l and lse =
+// ln 2 (m + log2 l): one pass over the cache.
 //
 // Every cached byte is read once and takes only heads/kv_heads products, so
 // HBM bandwidth bounds it (8 query heads to a cached bf16 head: 8 flops a byte,
 // 52 TFLOP/s at the measured 6.55 TB/s).  What counts is that all SMs read all
-// the time, whatever the lengths are:
+// the time, whatever the lengths are, and that the work per byte stays small:
 //   - The line of all tiles is cut evenly over the warps (cache_schedule.cuh).
 //   - A warp streams its piece through a ring of its own in shared memory
-//     (cp.async, one tile a stage), across the ends of segments, and waits for
-//     no other warp: the loop has no CTA barrier.
-//   - A tile's products run on mma.sync with the 16 rows of its A operand
-//     taken by the query heads that share the cached head.  The tcgen05 path
-//     would need 64 or 128 rows; 16 already hold the work well under the time
-//     that the bytes take.
-// Parts of segments that a cut falls into go to the workspace and are joined
-// by k_join; where a CTA's whole piece lies in one segment its warps join in
-// shared memory first.
+//     (cp.async, a unit being a tile's keys or its values), across the ends of
+//     segments, and waits for no other warp: the loop has no CTA barrier.
+//   - The products run on mma.sync with the TOKENS as the rows of the A operand
+//     (16) and the query heads of one cached head as the columns of B (8): up to
+//     8 heads fill it, where heads as rows would leave half of it or more empty,
+//     and the outputs take 8 columns of registers, so that 16 warps fit an SM.
+//     The tcgen05 path would need 64 or 128 rows of queries; a decode step has
+//     one to a few, and this holds the work well under the time of the bytes.
+// Parts of segments that a cut falls into are joined in the CTA where they lie
+// next to each other, the rest by k_join through the workspace.
 #pragma once
 #include <cuda_fp16.h>
+
+#include <atomic>
 
 #include "cache_schedule.cuh"
 #include "fwpkm_cache_internal.cuh"
@@ -30,13 +34,18 @@ namespace attend {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNegInf = -__builtin_huge_valf();
-// Fewer tiles than this are not worth a warp of their own.
-constexpr int kLeastTiles = 2;
+constexpr float kLeastFactor = 1.18e-38f;  // a factor that no score feels, but not 0
+// A score may exceed the reference by this (base 2) before the sums are scaled
+// to a new one: weights stay under 2^(kShift + kSlack).
+constexpr float kSlack = 6.f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const char *src, bool ok) {
   const int n = ok ? 16 : 0;  // 0: nothing is read, zeros are written
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const char *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -71,13 +80,11 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const unsigned (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const unsigned (&a)[4], unsigned b0,
-                                         unsigned b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// 2^x for x <= 0 or about so; results under 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -95,89 +102,241 @@ __device__ __forceinline__ unsigned e4m3_f16(unsigned v) {
       : "r"(v));
   return d;
 }
-// x as two TF32 parts: the rest beyond them is under 2^-22 of x.
-__device__ __forceinline__ void split_tf32(unsigned x, unsigned &hi, unsigned &lo) {
-  hi = (x + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+__device__ __forceinline__ unsigned transpose8(unsigned a) {  // of an 8 x 8 matrix of 16 bits
+  unsigned d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// log sum e^s from a reference and a sum in base 2.
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.f ? kNegInf : kLn2 * (m + log2f(l));
 }
 
 // ---------------------------------------------------------------------------
-// Element types.  Each says how a tile of TT tokens turns into scores and how
-// weights and the tile turn into outputs:
-//   s[TT/8][4]  scores; thread (g = lane/4, t = lane%4) holds rows g, g + 8 and
-//               tokens 8n + 2t, + 1, the accumulator layout of mma.m16n8
-//   o[DP/8][4]  outputs in the same layout; element (n, c) of row g is head
-//               element col(n) + c
+// Element types.  Each holds the queries, reference m, sum l and outputs o of
+// one segment, and works on a tile of TT tokens in two steps:
+//   scores(keys, visible)   weights 2^(c s - m) of the tile's tokens, kept
+//   outputs(values)         o += weights x values
+// Its outputs are kParts groups of 32 lanes x 4 floats; float e of group i
+// and a lane belongs to head head_of and head element col_of.
 // ---------------------------------------------------------------------------
+
+// What the two tensor-core types share.  Thread (g = lane/4, t = lane%4).  s
+// and p: tokens 16n + g (+ 8), heads 8h + 2t (+ 1), the accumulator layout of
+// mma.m16n8.  o: head elements as rows, heads as columns.
+template <typename Self, int DP_, int TT_, int NT_>
+struct Mma {
+  static constexpr int DP = DP_, TT = TT_, NT = NT_, HEADS = 8 * NT_;
+  static constexpr int kParts = DP / 16 * NT;
+  unsigned q[DP / 16][NT][2];
+  float c[NT][2], m[NT][2], l[NT][2];
+  float o[DP / 16][NT][4];
+  unsigned hi[TT / 16][NT][2];
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int h = 0; h < NT; ++h) {
+      m[h][0] = m[h][1] = kNegInf;
+      l[h][0] = l[h][1] = 0.f;
+#pragma unroll
+      for (int n = 0; n < DP / 16; ++n) o[n][h][0] = o[n][h][1] = o[n][h][2] = o[n][h][3] = 0.f;
+    }
+  }
+  // s: products; on return weights, in the same places.  kShift: the largest
+  // weight is 2^kShift when the reference is new.
+  __device__ __forceinline__ void weigh(float (&s)[TT / 16][NT][4], unsigned vis, float shift) {
+    const int g = (threadIdx.x & 31) >> 2;
+    if (vis != FULL) {
+#pragma unroll
+      for (int n = 0; n < TT / 16; ++n)
+#pragma unroll
+        for (int h = 0; h < NT; ++h) {
+          if (!((vis >> (16 * n + g)) & 1u)) s[n][h][0] = s[n][h][1] = kNegInf;
+          if (!((vis >> (16 * n + 8 + g)) & 1u)) s[n][h][2] = s[n][h][3] = kNegInf;
+        }
+    }
+    float top[NT][2];
+    bool over = false;
+#pragma unroll
+    for (int h = 0; h < NT; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(s[0][h][e], s[0][h][2 + e]);
+#pragma unroll
+        for (int n = 1; n < TT / 16; ++n) x = fmaxf(x, fmaxf(s[n][h][e], s[n][h][2 + e]));
+        top[h][e] = x;
+        over |= fmaf(x, c[h][e], -m[h][e]) > shift + kSlack;
+      }
+    if (__any_sync(FULL, over)) {
+#pragma unroll
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = top[h][e];
+          x = fmaxf(x, __shfl_xor_sync(FULL, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(FULL, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
+          x = fmaxf(m[h][e], fmaf(x, c[h][e], -shift));
+          const float f = ex2(m[h][e] - (x == kNegInf ? 0.f : x));
+          m[h][e] = x;
+          l[h][e] *= f;
+#pragma unroll
+          for (int n = 0; n < DP / 16; ++n) {
+            o[n][h][e] *= f;
+            o[n][h][2 + e] *= f;
+          }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < NT; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float u = m[h][e] == kNegInf ? 0.f : m[h][e];
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < TT / 16; ++n) {
+          s[n][h][e] = ex2(fmaf(s[n][h][e], c[h][e], -u));
+          s[n][h][2 + e] = ex2(fmaf(s[n][h][2 + e], c[h][e], -u));
+          sum += s[n][h][e] + s[n][h][2 + e];
+        }
+        l[h][e] += sum;
+      }
+  }
+  // The warp's l: each thread has summed its own tokens.
+  __device__ __forceinline__ void total() {
+#pragma unroll
+    for (int h = 0; h < NT; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[h][e] += __shfl_xor_sync(FULL, l[h][e], 4);
+        l[h][e] += __shfl_xor_sync(FULL, l[h][e], 8);
+        l[h][e] += __shfl_xor_sync(FULL, l[h][e], 16);
+      }
+  }
+  __device__ __forceinline__ float4 part(int i) const {
+    const float(&x)[4] = o[i / NT][i % NT];
+    return make_float4(x[0], x[1], x[2], x[3]);
+  }
+  // f(head, m, l) once for each head
+  template <typename F>
+  __device__ __forceinline__ void stats(F &&f) const {
+    if ((threadIdx.x & 31) < 4)
+#pragma unroll
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) f(8 * h + 2 * (threadIdx.x & 3) + e, m[h][e], l[h][e]);
+  }
+  __device__ __forceinline__ static int head_of(int i, int lane, int e) {
+    return 8 * (i % NT) + 2 * (lane & 3) + (e & 1);
+  }
+  __device__ __forceinline__ static int col_of(int i, int lane, int e) {
+    return i / NT * 16 + Self::row_elem((lane >> 2) + 8 * (e >> 1));
+  }
+  // The segment's result; vs: the values' scale.
+  __device__ __forceinline__ void finish(__nv_bfloat16 *out, float *lse, int rows, int dim,
+                                         float vs) {
+    total();
+    float inv[NT][2];
+#pragma unroll
+    for (int h = 0; h < NT; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) inv[h][e] = l[h][e] == 0.f ? 0.f : vs / l[h][e];
+    static_cast<Self *>(this)->write(out, rows, dim, inv);
+    if (lse)
+      stats([&](int h, float mh, float lh) {
+        if (h < rows) lse[h] = log_sum(mh, lh);
+      });
+  }
+};
 
 // bf16: weights go in as two bf16 parts, so that rounding them costs nothing
 // of the result's accuracy (one part alone would add an error of the size of
 // the final rounding).  The second product is hidden behind the loads.
-template <int DP_, int TT_>
-struct Bf16 {
-  static constexpr int DP = DP_, TT = TT_, ESZ = 2, PITCH = DP * 2 + 16, QSMEM = 0;
-  static constexpr float kShift = 0.f;
-  unsigned q[DP / 16][4];
+template <int DP_, int TT_, int NT_>
+struct Bf16 : Mma<Bf16<DP_, TT_, NT_>, DP_, TT_, NT_> {
+  using B = Mma<Bf16<DP_, TT_, NT_>, DP_, TT_, NT_>;
+  using Out = __nv_bfloat16;
+  static constexpr int DP = DP_, TT = TT_, NT = NT_, ESZ = 2, PITCH = DP * 2 + 16;
+  static constexpr int kDtype = FWPKM_BF16;
+  unsigned lo[TT / 16][NT][2];
 
-  __device__ __forceinline__ void load_q(const char *qp, int rows, int dim, uint32_t) {
+  // Head element of row r of an output tile's 16.
+  __device__ __forceinline__ static int row_elem(int r) { return r; }
+  __device__ __forceinline__ void load_q(const char *qp, int rows, int dim, float f) {
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+    const unsigned flip = f < 0.f ? 0x80008000u : 0u;
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = g + (i & 1) * 8, c = k * 16 + t * 2 + (i >> 1) * 8;
-        q[k][i] = row < rows && c < dim
-                      ? __ldg(reinterpret_cast<const unsigned *>(qp + ((int64_t)row * dim + c) * 2))
-                      : 0u;
-      }
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = 8 * h + g, c = k * 16 + t * 2 + i * 8;
+          this->q[k][h][i] =
+              row < rows && c < dim
+                  ? flip ^ __ldg(reinterpret_cast<const unsigned *>(qp + (row * dim + c) * 2))
+                  : 0u;
+        }
+#pragma unroll
+    for (int h = 0; h < NT; ++h) this->c[h][0] = this->c[h][1] = fmaxf(fabsf(f), kLeastFactor);
   }
-  __device__ __forceinline__ void scores(float (&s)[TT / 8][4], uint32_t ks, uint32_t) {
-    const int l = threadIdx.x & 31;
-    const uint32_t a0 = ks + ((l & 7) + (l >> 4) * 8) * PITCH + ((l >> 3) & 1) * 16;
+  __device__ __forceinline__ void scores(uint32_t ks, unsigned vis) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t a0 = ks + ((lane & 7) + ((lane >> 3) & 1) * 8) * PITCH + (lane >> 4) * 16;
+    float s[TT / 16][NT][4] = {};
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
       for (int n = 0; n < TT / 16; ++n) {
-        unsigned b[4];
-        ldsm4(b, a0 + n * 16 * PITCH + k * 32);
-        mma_bf16(s[2 * n], q[k], b[0], b[1]);
-        mma_bf16(s[2 * n + 1], q[k], b[2], b[3]);
+        unsigned a[4];
+        ldsm4(a, a0 + n * 16 * PITCH + k * 32);
+#pragma unroll
+        for (int h = 0; h < NT; ++h) mma_bf16(s[n][h], a, this->q[k][h][0], this->q[k][h][1]);
       }
+    this->weigh(s, vis, 0.f);
+#pragma unroll
+    for (int n = 0; n < TT / 16; ++n)
+#pragma unroll
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float x = s[n][h][2 * i], y = s[n][h][2 * i + 1];
+          const unsigned w = pack_bf16(x, y);
+          this->hi[n][h][i] = transpose8(w);
+          lo[n][h][i] = transpose8(
+              pack_bf16(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u)));
+        }
   }
-  __device__ __forceinline__ void outputs(float (&o)[DP / 8][4], const float (&p)[TT / 8][4],
-                                          uint32_t vs) {
-    const int l = threadIdx.x & 31;
-    const uint32_t a0 = vs + (l & 15) * PITCH + (l >> 4) * 16;
+  __device__ __forceinline__ void outputs(uint32_t vs) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t a0 = vs + ((lane & 7) + (lane >> 4) * 8) * PITCH + ((lane >> 3) & 1) * 16;
 #pragma unroll
-    for (int k = 0; k < TT / 16; ++k) {
-      unsigned hi[4], lo[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = p[2 * k + (i >> 1)][(i & 1) * 2], y = p[2 * k + (i >> 1)][(i & 1) * 2 + 1];
-        hi[i] = pack_bf16(x, y);
-        lo[i] = pack_bf16(x - __uint_as_float(hi[i] << 16),
-                          y - __uint_as_float(hi[i] & 0xffff0000u));
-      }
+    for (int k = 0; k < TT / 16; ++k)
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) {
-        unsigned b[4];
-        ldsm4t(b, a0 + k * 16 * PITCH + n * 32);
-        mma_bf16(o[2 * n], hi, b[0], b[1]);
-        mma_bf16(o[2 * n + 1], hi, b[2], b[3]);
-        mma_bf16(o[2 * n], lo, b[0], b[1]);
-        mma_bf16(o[2 * n + 1], lo, b[2], b[3]);
-      }
-    }
-  }
-  // f(row half, first column, values of two neighbouring columns)
-  template <typename F>
-  __device__ __forceinline__ static void each(const float (&o)[DP / 8][4], F &&f) {
-    const int t = threadIdx.x & 3;
+        unsigned a[4];
+        ldsm4t(a, a0 + k * 16 * PITCH + n * 32);
 #pragma unroll
-    for (int n = 0; n < DP / 8; ++n) {
-      f(0, n * 8 + t * 2, o[n][0], o[n][1]);
-      f(1, n * 8 + t * 2, o[n][2], o[n][3]);
-    }
+        for (int h = 0; h < NT; ++h) {
+          mma_bf16(this->o[n][h], a, this->hi[k][h][0], this->hi[k][h][1]);
+          mma_bf16(this->o[n][h], a, lo[k][h][0], lo[k][h][1]);
+        }
+      }
+  }
+  // The finished rows: out + row * dim, for the block's first `rows` heads.
+  __device__ __forceinline__ void write(Out *out, int rows, int dim, const float (&inv)[NT][2]) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll
+    for (int n = 0; n < DP / 16; ++n)
+#pragma unroll
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const unsigned w = transpose8(pack_bf16(this->o[n][h][2 * i] * inv[h][0],
+                                                  this->o[n][h][2 * i + 1] * inv[h][1]));
+          const int row = 8 * h + g, c = n * 16 + i * 8 + t * 2;
+          if (row < rows && c < dim) *reinterpret_cast<unsigned *>(out + row * dim + c) = w;
+        }
   }
 };
 
@@ -185,265 +344,377 @@ struct Bf16 {
 // those.  A row of queries is scaled by a power of two so that its largest
 // element lies in [1, 2): what a bf16 element then loses to the 16-bit range is
 // under 2^-25 of the largest, no more than the 32-bit sum.  Weights are held
-// 2^12 too large (kShift), which keeps all down to 2^-26 of the largest above
+// 2^8 too large (kShift), which keeps all down to 2^-22 of the largest above
 // the 16-bit format's smallest normal number; at 11 bits their rounding is an
 // eighth of the result's.
 // ldmatrix moves pairs of 8-bit elements: a lane gets 4 neighbouring elements
-// of a token, taken as elements 2t, 2t+1, 2t+8, 2t+9 of the product's 16; the
-// queries are loaded in the same order, the outputs come out in it.
-template <int DP_, int TT_>
-struct E4m3 {
-  static constexpr int DP = DP_, TT = TT_, ESZ = 1, PITCH = DP + 16, QSMEM = 0;
-  static constexpr float kShift = 12.f;
-  unsigned q[DP / 16][4];
+// of a token's keys, taken as elements 2t, 2t+1, 2t+8, 2t+9 of the product's
+// 16 (the queries are loaded in the same order), and 2 neighbouring elements of
+// two tokens' values, which become rows g and g + 8 of the outputs.
+template <int DP_, int TT_, int NT_>
+struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
+  using B = Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_>;
+  using Out = __nv_bfloat16;
+  static constexpr int DP = DP_, TT = TT_, NT = NT_, ESZ = 1, PITCH = DP + 16;
+  static constexpr int kDtype = FWPKM_E4M3;
+  static constexpr float kShift = 8.f;
 
-  float f0, f1;  // the powers of two taken out of rows g and g + 8
-  __device__ __forceinline__ void load_q(const char *qp, int rows, int dim, uint32_t) {
-    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-    float top[2] = {0.f, 0.f};
+  __device__ __forceinline__ static int row_elem(int r) { return (r & 7) * 2 + (r >> 3); }
+  __device__ __forceinline__ void load_q(const char *qp, int rows, int dim, float f) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int k = 0; k < DP / 16; ++k)
+    for (int h = 0; h < NT; ++h) {
+      float top = 0.f;
+      const int row = 8 * h + g;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = g + r * 8, c = k * 16 + t * 4;
+      for (int k = 0; k < DP / 16; ++k) {
+        const int c = k * 16 + t * 4;
         uint2 v = make_uint2(0u, 0u);
         if (row < rows && c < dim)
-          v = __ldg(reinterpret_cast<const uint2 *>(qp + ((int64_t)row * dim + c) * 2));
-        q[k][r] = v.x;
-        q[k][2 + r] = v.y;
+          v = __ldg(reinterpret_cast<const uint2 *>(qp + (row * dim + c) * 2));
+        this->q[k][h][0] = v.x;
+        this->q[k][h][1] = v.y;
         const float m0 = fmaxf(fabsf(__uint_as_float(v.x << 16)),
                                fabsf(__uint_as_float(v.x & 0xffff0000u)));
         const float m1 = fmaxf(fabsf(__uint_as_float(v.y << 16)),
                                fabsf(__uint_as_float(v.y & 0xffff0000u)));
-        top[r] = fmaxf(top[r], fmaxf(m0, m1));
+        top = fmaxf(top, fmaxf(m0, m1));
       }
-    float down[2], up[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 1));
-      top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 2));
+      top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
       // 2^-e and 2^e, e the exponent of the largest element kept where both
       // are normal numbers (a row of zeros, or one with infinities: 1)
-      int e = (int)((__float_as_uint(top[r]) >> 23) & 255u);
+      int e = (int)((__float_as_uint(top) >> 23) & 255u);
       e = e == 0 || e == 255 ? 127 : e < 2 ? 2 : e > 252 ? 252 : e;
-      down[r] = __uint_as_float((unsigned)(254 - e) << 23);
-      up[r] = __uint_as_float((unsigned)e << 23);
+      const float down =
+          __uint_as_float(((unsigned)(254 - e) << 23) | (f < 0.f ? 0x80000000u : 0u));
+      const float up = __uint_as_float((unsigned)e << 23);
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          this->q[k][h][i] = pack_f16(__uint_as_float(this->q[k][h][i] << 16) * down,
+                                      __uint_as_float(this->q[k][h][i] & 0xffff0000u) * down);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)  // the factors of this thread's columns
+        this->c[h][i] =
+            fmaxf(fabsf(f) * __shfl_sync(FULL, up, (2 * t + i) * 4), kLeastFactor);
     }
-#pragma unroll
-    for (int k = 0; k < DP / 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        q[k][i] = pack_f16(__uint_as_float(q[k][i] << 16) * down[i & 1],
-                           __uint_as_float(q[k][i] & 0xffff0000u) * down[i & 1]);
-    f0 = up[0];
-    f1 = up[1];
   }
-  __device__ __forceinline__ void scores(float (&s)[TT / 8][4], uint32_t ks, uint32_t) {
-    const int l = threadIdx.x & 31;
-    const uint32_t a0 = ks + ((l & 7) + (l >> 4) * 8) * PITCH + ((l >> 3) & 1) * 16;
-    // four matrices: 16 tokens x two groups of 16 elements
+  __device__ __forceinline__ void scores(uint32_t ks, unsigned vis) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t a0 = ks + ((lane & 7) + ((lane >> 3) & 1) * 8) * PITCH + (lane >> 4) * 16;
+    float s[TT / 16][NT][4] = {};
 #pragma unroll
     for (int k = 0; k < DP / 32; ++k)
 #pragma unroll
       for (int n = 0; n < TT / 16; ++n) {
-        unsigned b[4];
+        unsigned b[4];  // tokens 0-7 and 8-15 of 16 elements, then of the next 16
         ldsm4(b, a0 + n * 16 * PITCH + k * 32);
-        mma_f16(s[2 * n], q[2 * k], e4m3_f16(b[0]), e4m3_f16(b[0] >> 16));
-        mma_f16(s[2 * n + 1], q[2 * k], e4m3_f16(b[2]), e4m3_f16(b[2] >> 16));
-        mma_f16(s[2 * n], q[2 * k + 1], e4m3_f16(b[1]), e4m3_f16(b[1] >> 16));
-        mma_f16(s[2 * n + 1], q[2 * k + 1], e4m3_f16(b[3]), e4m3_f16(b[3] >> 16));
-      }
 #pragma unroll
-    for (int n = 0; n < TT / 8; ++n) {
-      s[n][0] *= f0;
-      s[n][1] *= f0;
-      s[n][2] *= f1;
-      s[n][3] *= f1;
-    }
-  }
-  __device__ __forceinline__ void outputs(float (&o)[DP / 8][4], const float (&p)[TT / 8][4],
-                                          uint32_t vs) {
-    const int l = threadIdx.x & 31;
-    const uint32_t a0 = vs + (l & 15) * PITCH + (l >> 4) * 16;
+        for (int j = 0; j < 2; ++j) {
+          const unsigned a[4] = {e4m3_f16(b[2 * j]), e4m3_f16(b[2 * j + 1]),
+                                 e4m3_f16(b[2 * j] >> 16), e4m3_f16(b[2 * j + 1] >> 16)};
 #pragma unroll
-    for (int k = 0; k < TT / 16; ++k) {
-      unsigned w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = pack_f16(p[2 * k + (i >> 1)][(i & 1) * 2], p[2 * k + (i >> 1)][(i & 1) * 2 + 1]);
-#pragma unroll
-      for (int n = 0; n < DP / 32; ++n) {
-        unsigned b[4];
-        // matrices: tokens 0-7 and 8-15 of element pairs 32n .. +15, then +16 .. +31
-        ldsm4t(b, a0 + k * 16 * PITCH + n * 32);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // bytes (t, 2g) (t, 2g+1) (t+1, 2g) (t+1, 2g+1): sort by element
-          const unsigned x = __byte_perm(b[2 * h], 0, 0x3120);
-          const unsigned y = __byte_perm(b[2 * h + 1], 0, 0x3120);
-          mma_f16(o[4 * n + 2 * h], w, e4m3_f16(x), e4m3_f16(y));
-          mma_f16(o[4 * n + 2 * h + 1], w, e4m3_f16(x >> 16), e4m3_f16(y >> 16));
+          for (int h = 0; h < NT; ++h)
+            mma_f16(s[n][h], a, this->q[2 * k + j][h][0], this->q[2 * k + j][h][1]);
         }
       }
-    }
+    this->weigh(s, vis, kShift);
+#pragma unroll
+    for (int n = 0; n < TT / 16; ++n)
+#pragma unroll
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          this->hi[n][h][i] = transpose8(pack_f16(s[n][h][2 * i], s[n][h][2 * i + 1]));
   }
-  template <typename F>
-  __device__ __forceinline__ static void each(const float (&o)[DP / 8][4], F &&f) {
-    const int t = threadIdx.x & 3;
+  __device__ __forceinline__ void outputs(uint32_t vs) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t a0 = vs + (lane & 15) * PITCH + (lane >> 4) * 16;
+#pragma unroll
+    for (int k = 0; k < TT / 16; ++k)
+#pragma unroll
+      for (int n = 0; n < DP / 32; ++n) {
+        unsigned b[4];  // tokens 0-7 and 8-15 of 8 pairs of elements, then of the next 8
+        ldsm4t(b, a0 + k * 16 * PITCH + n * 32);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // bytes (t, 2g) (t, 2g+1) (t+1, 2g) (t+1, 2g+1): sort by element
+          const unsigned x = __byte_perm(b[2 * j], 0, 0x3120);
+          const unsigned y = __byte_perm(b[2 * j + 1], 0, 0x3120);
+          const unsigned a[4] = {e4m3_f16(x), e4m3_f16(x >> 16), e4m3_f16(y), e4m3_f16(y >> 16)};
+#pragma unroll
+          for (int h = 0; h < NT; ++h)
+            mma_f16(this->o[2 * n + j][h], a, this->hi[k][h][0], this->hi[k][h][1]);
+        }
+      }
+  }
+  __device__ __forceinline__ void write(Out *out, int rows, int dim, const float (&inv)[NT][2]) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
     for (int n = 0; n < DP / 16; ++n)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        f(0, n * 16 + t * 4 + c * 2, o[2 * n][c], o[2 * n + 1][c]);
-        f(1, n * 16 + t * 4 + c * 2, o[2 * n][2 + c], o[2 * n + 1][2 + c]);
+      for (int h = 0; h < NT; ++h) {
+        unsigned w[2];  // elements 4t, 4t + 2 and 4t + 1, 4t + 3 of the 16
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          w[i] = transpose8(pack_bf16(this->o[n][h][2 * i] * inv[h][0],
+                                      this->o[n][h][2 * i + 1] * inv[h][1]));
+        const int row = 8 * h + g, c = n * 16 + t * 4;
+        if (row < rows && c < dim)
+          *reinterpret_cast<uint2 *>(out + row * dim + c) =
+              make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632));
       }
   }
 };
 
-// f32: every product in three TF32 ones (high x high, high x low, low x high),
-// which leaves errors of 2^-22 of a term.  The queries lie in shared memory:
-// their parts would not fit the registers.  The tokens of a product's 8 are
-// taken in the order 0 2 4 6 1 3 5 7, so that a thread's scores are already
-// its share of the second product.
-template <int DP_, int TT_>
+// f32: the products run as plain 32-bit multiply-adds, which hold the full
+// accuracy; RR heads take RR of them an element, 8 flops a byte at 8 heads, a
+// third of what the SMs can do in the time of the bytes.  A lane has V = DP/32
+// elements of every head's query and output.  The tile's 8 x RR products of a
+// token and a head, each spread over the lanes, are summed by halving: 31
+// exchanges for 32 sums, after which lane i has sum i.
+template <int DP_, int RR_>
 struct F32 {
-  static constexpr int DP = DP_, TT = TT_, ESZ = 4, PITCH = DP * 4 + 16, QSMEM = 16 * PITCH;
-  static constexpr float kShift = 0.f;
-  static_assert(TT == 8, "one token tile of the product");
+  using Out = float;
+  static constexpr int DP = DP_, TT = 8, HEADS = RR_, RR = RR_, ESZ = 4, PITCH = DP * 4;
+  static constexpr int kDtype = FWPKM_F32;
+  static constexpr int V = DP / 32, NS = 8 * RR / 32;  // NS scores a lane
+  static constexpr int VP = V < 4 ? V : 4;             // elements of one shared load
+  static constexpr int kParts = RR * V / 4 > 0 ? (RR * V + 3) / 4 : 1;
+  static_assert(RR == 4 || RR == 8, "8 tokens x RR heads are whole warps of scores");
+  float q[RR][V], o[RR][V];
+  float c, m, l;  // of head lane % RR (each lane of a head: its own tokens' sum)
+  float p[NS];
 
-  __device__ __forceinline__ void load_q(const char *qp, int rows, int dim, uint32_t qs) {
-    __syncwarp();
-    for (int i = threadIdx.x & 31; i < 16 * (DP / 4); i += 32) {
-      const int row = i / (DP / 4), c = (i % (DP / 4)) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row < rows && c < dim)
-        v = __ldg(reinterpret_cast<const float4 *>(qp + ((int64_t)row * dim + c) * 4));
-      asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(qs + row * PITCH + c * 4),
-                   "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                   : "memory");
-    }
-    __syncwarp();
+  // Elements of this lane: VP consecutive ones, then the same 128 further on.
+  __device__ __forceinline__ static int elem(int lane, int v) {
+    return (v / VP) * 32 * VP + lane * VP + v % VP;
   }
-  __device__ __forceinline__ void scores(float (&s)[1][4], uint32_t ks, uint32_t qs) {
-    const int l = threadIdx.x & 31;
-    const uint32_t kb = ks + (l & 7) * PITCH + (l >> 3) * 16;
-    const uint32_t qb = qs + ((l & 7) + ((l >> 3) & 1) * 8) * PITCH + (l >> 4) * 16;
-    float x[4] = {0.f, 0.f, 0.f, 0.f};  // the cross terms
-#pragma unroll 4
-    for (int k = 0; k < DP / 16; ++k) {
-      unsigned b[4];
-      ldsm4(b, kb + k * 64);
+  __device__ __forceinline__ void reset() {
+    m = kNegInf;
+    l = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        unsigned a[4], ah[4], al[4], bh0, bl0, bh1, bl1;
-        ldsm4(a, qb + k * 64 + h * 32);
+    for (int h = 0; h < RR; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split_tf32(a[i], ah[i], al[i]);
-        split_tf32(b[2 * h], bh0, bl0);
-        split_tf32(b[2 * h + 1], bh1, bl1);
-        mma_tf32(x, al, bh0, bh1);
-        mma_tf32(x, ah, bl0, bl1);
-        mma_tf32(s[0], ah, bh0, bh1);
+      for (int v = 0; v < V; ++v) o[h][v] = 0.f;
+  }
+  __device__ __forceinline__ void load_q(const char *qp, int rows, int dim, float f) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < RR; ++h)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = elem(lane, v);
+        const float x =
+            h < rows && e < dim ? __ldg(reinterpret_cast<const float *>(qp) + h * dim + e) : 0.f;
+        q[h][v] = f < 0.f ? -x : x;
+      }
+    c = fmaxf(fabsf(f), kLeastFactor);
+  }
+  __device__ __forceinline__ static void row(float (&x)[V], uint32_t a) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < V / VP; ++i) {
+      const uint32_t at = a + (i * 32 + lane) * VP * 4;
+      if constexpr (VP == 4)
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(x[i * 4]), "=f"(x[i * 4 + 1]), "=f"(x[i * 4 + 2]), "=f"(x[i * 4 + 3])
+                     : "r"(at)
+                     : "memory");
+      else
+        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
+                     : "=f"(x[i * 2]), "=f"(x[i * 2 + 1])
+                     : "r"(at)
+                     : "memory");
+    }
+  }
+  __device__ __forceinline__ void scores(uint32_t ks, unsigned vis) {
+    const int lane = threadIdx.x & 31;
+    constexpr int TS = 32 / RR;  // tokens whose products make 32 sums
+    float s[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      float x[32];
+#pragma unroll
+      for (int t = 0; t < TS; ++t) {
+        float k[V];
+        row(k, ks + (j * TS + t) * PITCH);
+#pragma unroll
+        for (int h = 0; h < RR; ++h) {
+          float a = q[h][0] * k[0];
+#pragma unroll
+          for (int v = 1; v < V; ++v) a = fmaf(q[h][v], k[v], a);
+          x[t * RR + h] = a;
+        }
+      }
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+          const float keep = up ? x[i + w] : x[i], give = up ? x[i] : x[i + w];
+          x[i] = keep + __shfl_xor_sync(FULL, give, w);
+        }
+      }
+      s[j] = (vis >> (j * TS + lane / RR)) & 1u ? x[0] : kNegInf;
+    }
+    float top = s[0];
+#pragma unroll
+    for (int j = 1; j < NS; ++j) top = fmaxf(top, s[j]);
+    if (__any_sync(FULL, fmaf(top, c, -m) > kSlack)) {
+#pragma unroll
+      for (int w = RR; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, w));
+      top = fmaxf(m, top * c);
+      const float f = ex2(m - (top == kNegInf ? 0.f : top));
+      m = top;
+      l *= f;
+#pragma unroll
+      for (int h = 0; h < RR; ++h) {
+        const float fh = __shfl_sync(FULL, f, h);
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[h][v] *= fh;
       }
     }
+    const float u = m == kNegInf ? 0.f : m;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[0][i] += x[i];
-  }
-  __device__ __forceinline__ void outputs(float (&o)[DP / 8][4], const float (&p)[1][4],
-                                          uint32_t vs) {
-    const int l = threadIdx.x & 31;
-    const uint32_t a0 = vs + (l & 3) * 2 * PITCH + (l >> 2) * 4;
-    unsigned wh[4], wl[4];
-    split_tf32(__float_as_uint(p[0][0]), wh[0], wl[0]);
-    split_tf32(__float_as_uint(p[0][2]), wh[1], wl[1]);
-    split_tf32(__float_as_uint(p[0][1]), wh[2], wl[2]);
-    split_tf32(__float_as_uint(p[0][3]), wh[3], wl[3]);
-#pragma unroll
-    for (int n = 0; n < DP / 8; ++n) {
-      unsigned b0, b1, bh0, bl0, bh1, bl1;
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b0) : "r"(a0 + n * 32) : "memory");
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b1) : "r"(a0 + PITCH + n * 32) : "memory");
-      split_tf32(b0, bh0, bl0);
-      split_tf32(b1, bh1, bl1);
-      mma_tf32(o[n], wl, bh0, bh1);
-      mma_tf32(o[n], wh, bl0, bl1);
-      mma_tf32(o[n], wh, bh0, bh1);
+    for (int j = 0; j < NS; ++j) {
+      p[j] = ex2(fmaf(s[j], c, -u));
+      l += p[j];
     }
+  }
+  __device__ __forceinline__ void outputs(uint32_t vs) {
+    constexpr int TS = 32 / RR;
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int t = 0; t < TS; ++t) {
+        float x[V];
+        row(x, vs + (j * TS + t) * PITCH);
+#pragma unroll
+        for (int h = 0; h < RR; ++h) {
+          const float w = __shfl_sync(FULL, p[j], t * RR + h);
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[h][v] = fmaf(w, x[v], o[h][v]);
+        }
+      }
+  }
+  __device__ __forceinline__ void total() {
+#pragma unroll
+    for (int w = RR; w < 32; w <<= 1) l += __shfl_xor_sync(FULL, l, w);
+  }
+  __device__ __forceinline__ float4 part(int i) const {
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = o[(i * 4 + e) / V][(i * 4 + e) % V];
+    return make_float4(x[0], x[1], x[2], x[3]);
   }
   template <typename F>
-  __device__ __forceinline__ static void each(const float (&o)[DP / 8][4], F &&f) {
-    const int t = threadIdx.x & 3;
+  __device__ __forceinline__ void stats(F &&f) const {
+    if ((threadIdx.x & 31) < RR) f(threadIdx.x & 31, m, l);
+  }
+  __device__ __forceinline__ static int head_of(int i, int, int e) { return (i * 4 + e) / V; }
+  __device__ __forceinline__ static int col_of(int i, int lane, int e) {
+    return elem(lane, (i * 4 + e) % V);
+  }
+  __device__ __forceinline__ void finish(float *out, float *lse, int rows, int dim, float vs) {
+    total();
+    const int lane = threadIdx.x & 31;
+    const float inv = l == 0.f ? 0.f : vs / l;
 #pragma unroll
-    for (int n = 0; n < DP / 8; ++n) {
-      f(0, n * 8 + t * 2, o[n][0], o[n][1]);
-      f(1, n * 8 + t * 2, o[n][2], o[n][3]);
+    for (int h = 0; h < RR; ++h) {
+      const float f = __shfl_sync(FULL, inv, h);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = elem(lane, v);
+        if (h < rows && e < dim) out[h * dim + e] = o[h][v] * f;
+      }
     }
+    if (lse && lane < rows) lse[lane] = log_sum(m, l);
   }
 };
 
 // ---------------------------------------------------------------------------
 
-// Length of sequence b within what the table can hold.
-__device__ __forceinline__ int length_of(const AttendArgs &a, int b, bool &bad) {
-  return cache_length(__ldg(a.s.lengths + b), a.s.table_width, a.p.page_size, bad);
-}
-
-// A place on the line of tiles.
-struct Cursor {
-  int b, hr, tile;  // sequence, cached head * blocks + row block, tile of the segment
-  Span s;
-  __device__ __forceinline__ void enter(const AttendArgs &a, int tile_tokens) {
-    bool bad;
-    s = cache_span(length_of(a, b, bad), a.window, tile_tokens);
+// Lengths of the sequences within what the table can hold: those that fit lie
+// in shared memory.
+struct Lengths {
+  const AttendArgs &a;
+  const int *kept;
+  int keep;
+  __device__ __forceinline__ static int get(const AttendArgs &a, int b, bool &bad) {
+    return cache_length(__ldg(a.s.lengths + b), a.s.table_width, a.p.page_size, bad);
   }
-  __device__ __forceinline__ void next(const AttendArgs &a, int tile_tokens) {
-    if (++tile < s.count) return;
+  __device__ __forceinline__ int operator()(int b) const {
+    bool bad;
+    return b < keep ? kept[b] : get(a, b, bad);
+  }
+};
+
+// A tile's place on the line.
+struct Cursor {
+  int b, hr, tile;  // sequence, cached head * blocks + block, tile of the segment
+  Span s;
+  __device__ __forceinline__ void enter(const Lengths &len, int tile_tokens) {
+    s = cache_span(len(b), len.a.window, tile_tokens);
+  }
+  // To the next tile; returns how many units further it is.
+  __device__ __forceinline__ int next(const Lengths &len, int tile_tokens) {
+    if (++tile < s.count) return tile == 1 ? kSegmentUnits + 1 : 1;
+    const int step = s.count == 1 ? kSegmentUnits + 1 : 1;
     tile = 0;
-    if (++hr < a.p.kv_heads * a.blocks) return;
-    hr = 0;
-    if (++b < a.s.B) enter(a, tile_tokens);
+    if (++hr == len.a.p.kv_heads * len.a.blocks) {
+      hr = 0;
+      if (++b < len.a.s.B) enter(len, tile_tokens);
+    }
+    return step;
   }
 };
 
 template <typename T>
-__device__ __forceinline__ void store2(char *p, float x, float y);
+__device__ __forceinline__ T to_out(float x);
 template <>
-__device__ __forceinline__ void store2<float>(char *p, float x, float y) {
-  *reinterpret_cast<float2 *>(p) = make_float2(x, y);
-}
+__device__ __forceinline__ float to_out<float>(float x) { return x; }
 template <>
-__device__ __forceinline__ void store2<__nv_bfloat16>(char *p, float x, float y) {
-  *reinterpret_cast<unsigned *>(p) = pack_bf16(x, y);
+__device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
 }
 
-template <typename TY, int WARPS, int STAGES>
+template <typename TY, int WARPS, int UNITS>
 struct Layout {
-  static constexpr int kTile = TY::TT * TY::PITCH;  // keys, then values
-  static constexpr int kStage = 2 * kTile;
-  static constexpr int kRing = STAGES * kStage;
-  static constexpr int kWarp = kRing + TY::QSMEM;
-  static constexpr int kJoinPitch = TY::DP + 8;  // floats: rows 8 banks apart
-  static constexpr int kSmem = WARPS * kWarp;
-  static_assert(kRing >= kAttendRows * kJoinPitch * 4, "a warp's sums fit its ring");
+  static constexpr int kUnit = TY::TT * TY::PITCH;  // a tile's keys, or its values
+  static constexpr int kRing = UNITS * kUnit;
+  static constexpr int kSmem = WARPS * kRing;
+  static constexpr int kPart = TY::kParts * 128;  // floats of a part
+  static_assert(kRing >= kPart * 4, "a warp's sums fit its ring");
   static_assert(kSmem <= 222 * 1024, "shared memory of an SM, less the static part");
 };
 
-template <typename TY, typename TO, int WARPS, int STAGES>
+template <typename TY, int WARPS, int UNITS>
 __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant__ AttendArgs a) {
-  using L = Layout<TY, WARPS, STAGES>;
-  constexpr int DP = TY::DP, TT = TY::TT, ESZ = TY::ESZ;
+  using L = Layout<TY, WARPS, UNITS>;
+  using Out = typename TY::Out;
+  constexpr int TT = TY::TT, ESZ = TY::ESZ, HEADS = TY::HEADS;
   extern __shared__ __align__(128) char smem[];
-  __shared__ long long before[WARPS * 32 + 1];  // tiles before each thread's sequences
+  __shared__ long long before[WARPS * 32 + 1];  // units before each thread's sequences
   __shared__ long long wsum[WARPS];
-  __shared__ unsigned bits[WARPS][STAGES];       // visible tokens of a stage's tile
-  __shared__ float2 jml[WARPS][kAttendRows];
+  __shared__ int kept[WARPS * 32];  // lengths of the first sequences
+  __shared__ unsigned bits[WARPS][UNITS];  // visible tokens of the tile whose keys are there
+  __shared__ long long last_seg[WARPS];    // first unit of the segment a warp ended in, or -1
+  __shared__ int4 last_at[WARPS];  // (sequence, head and block, the segment's last warp, begins)
+  __shared__ float2 last_ml[WARPS][HEADS];
+  __shared__ float weight[WARPS][HEADS];
+  __shared__ float2 run_ml[WARPS][HEADS];
+  __shared__ float end_weight[WARPS][HEADS];
+  __shared__ int run_at[WARPS];
 
+  static_assert(WARPS <= 16, "a half warp sums over the warps");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2;
-  char *ring = smem + warp * L::kWarp;
-  const uint32_t ring_u = smem_u32(ring), qs = ring_u + L::kRing;
+  char *ring = smem + warp * L::kRing;
+  const uint32_t ring_u = smem_u32(ring);
 
-  if (a.p.dim < DP) {  // elements behind the head's own: zeros, which no copy touches
+  if (a.p.dim < TY::DP) {  // elements behind the head's own: zeros, which no copy touches
     for (int i = lane; i < L::kRing / 16; i += 32)
       reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncwarp();
@@ -451,7 +722,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   griddep_wait();
   griddep_launch();
 
-  // ---- the line of tiles, and this warp's piece of it ---------------------
+  // ---- the line of units, and this warp's piece of it ---------------------
   const int chunk = (a.s.B + WARPS * 32 - 1) / (WARPS * 32);
   const int hrs = a.p.kv_heads * a.blocks;
   {
@@ -460,9 +731,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
       const int b = threadIdx.x * chunk + i;
       if (b >= a.s.B) break;
       bool bad;
-      const int len = length_of(a, b, bad);
+      const int len = Lengths::get(a, b, bad);
       if (bad && blockIdx.x == 0 && a.errors) atomicOr(a.errors, (unsigned)FWPKM_CACHE_BAD_LENGTH);
-      mine += cache_span(len, a.window, TT).count;
+      if (b < WARPS * 32) kept[b] = len;
+      mine += segment_units(cache_span(len, a.window, TT).count);
     }
     mine *= hrs;
     long long sum = mine;
@@ -473,363 +745,467 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
     }
     if (lane == 31) wsum[warp] = sum;
     __syncthreads();
-    long long base = 0;
-    for (int w = 0; w < warp; ++w) base += wsum[w];
+    long long base = lane < warp ? wsum[lane] : 0;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) base += __shfl_xor_sync(FULL, base, o);
+    base = __shfl_sync(FULL, base, 0);
     before[threadIdx.x] = base + sum - mine;
     if (threadIdx.x == WARPS * 32 - 1) before[WARPS * 32] = base + sum;
     __syncthreads();
   }
-  const long long total = before[WARPS * 32];
-  const int warps = cache_warps(total, gridDim.x * WARPS, kLeastTiles);
-  const int w = blockIdx.x * WARPS + warp;
-  const int wa = min(blockIdx.x * WARPS, warps), wb = min(wa + WARPS, warps);
-  const long long cta0 = cache_cut(total, warps, wa), cta1 = cache_cut(total, warps, wb);
-  const long long t0 = w < warps ? cache_cut(total, warps, w) : total;
-  const long long t1 = w < warps ? cache_cut(total, warps, w + 1) : total;
+  const Lengths lengths{a, kept, WARPS * 32};
+  const Line line = cache_line(before[WARPS * 32], gridDim.x * WARPS);
+  const int per = line_per_cta(line, gridDim.x);  // pieces of a CTA
+  const int w0 = blockIdx.x * per, w = w0 + warp;
+  const bool busy = warp < per && w < line.warps;
+  const long long u0 = busy ? line_cut(line, w) : 0;
+  const long long u1 = busy ? line_cut(line, w + 1) : 0;
 
-  Cursor at{};        // the tile that is computed
-  long long seg = 0;  // first tile of its segment
-  if (t0 < t1) {
-    int i = 0;  // the thread whose sequences t0 falls into
-    for (int j = lane; j < WARPS * 32; j += 32) i += before[j + 1] <= t0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) i += __shfl_xor_sync(FULL, i, o);
+  Cursor at{};          // the tile that is computed
+  long long unit = u1;  // its unit; from u1 on there is none
+  if (busy) {
+    // the thread whose sequences u0 falls into: the last one with so many before it
+    int i = 0;
+    if (WARPS > 1) i = __popc(__ballot_sync(FULL, lane < WARPS && before[lane * 32] <= u0)) - 1;
+    i = i * 32 + __popc(__ballot_sync(FULL, before[i * 32 + lane] <= u0)) - 1;
     long long p = before[i];
     at.b = i * chunk;
-    at.enter(a, TT);
-    while (p + (long long)at.s.count * hrs <= t0) {
-      p += (long long)at.s.count * hrs;
+    at.enter(lengths, TT);
+    while (p + segment_units(at.s.count) * hrs <= u0) {
+      p += segment_units(at.s.count) * hrs;
       ++at.b;
-      at.enter(a, TT);
+      at.enter(lengths, TT);
     }
-    at.hr = (int)((t0 - p) / at.s.count);
-    at.tile = (int)((t0 - p) - (long long)at.hr * at.s.count);
-    seg = t0 - at.tile;
+    const long long n = segment_units(at.s.count);
+    at.hr = (int)((u0 - p) / n);
+    p += at.hr * n;
+    at.tile = tile_from(u0 - p);
+    unit = p + tile_unit(at.tile);
+    if (at.tile >= at.s.count) {  // behind the segment's last tile: the next segment
+      unit = p + n;
+      at.tile = at.s.count - 1;
+      at.next(lengths, TT);
+    }
   }
-  // the whole piece of the CTA lies in one segment (all its warps agree)
-  const bool joined = cta0 < cta1 && (t0 >= t1 || (seg <= cta0 && seg + at.s.count >= cta1));
-  // a warp without tiles cannot tell, and has no part in either case
+
+  // the segment that the CTA's first warp is in the middle of: k_join's CTAs share it
+  if (threadIdx.x == 0) {
+    int4 id = make_int4(0, 0, -1, 0);
+    if (unit < u1 && at.tile > 0) {
+      const long long s = unit - tile_unit(at.tile);
+      id = make_int4(at.b, at.hr, line_owner(line, s + tile_unit(at.s.count - 1)),
+                     line_owner(line, s));
+    }
+    a.middles[blockIdx.x] = id;
+  }
 
   // ---- loads ---------------------------------------------------------------
-  constexpr int CPR = DP * ESZ / 16;  // 16-byte pieces of a padded row
+  constexpr int CPR = TY::DP * ESZ / 16;    // 16-byte pieces of a padded row
+  constexpr int kCopies = TT * CPR / 32;    // instructions a unit takes
+  constexpr int kRows = CPR <= 32 ? 32 / CPR : 1;  // rows an instruction copies,
+  constexpr int kSteps = CPR <= 32 ? 1 : CPR / 32;  // or instructions that a row takes
   const int cpr = a.p.dim * ESZ / 16;
-  Cursor ld = at;
-  int token = 0, page = -1;  // of this lane's row of the next tile to load
+  Cursor ld = at;          // the tile that is loaded
+  long long ld_unit = unit;
+  int token = 0, page = -1;  // of this lane's row
   bool seen = false;
   auto look = [&] {
     token = (ld.s.first + ld.tile) * TT + (lane % TT);
     seen = token >= ld.s.lo && token < ld.s.len;
-    page = seen ? __ldg(a.s.table + ld.b * a.s.table_stride + token / a.p.page_size) : -1;
+    page = seen ? __ldg(a.s.table + ld.b * a.s.table_stride + page_of(a.div, token)) : -1;
   };
-  auto load = [&](int stage) {
-    const bool ok = seen && (unsigned)page < (unsigned)a.p.pages;
-    if (seen && !ok && a.errors && lane < TT) atomicOr(a.errors, (unsigned)FWPKM_CACHE_BAD_PAGE);
-    const unsigned vis = __ballot_sync(FULL, ok);
-    if (lane == 0) bits[warp][stage] = vis;
-    const int64_t off = ok ? page * a.p.page_stride +
-                                 (int64_t)(ld.hr / a.blocks) * a.p.head_stride +
-                                 (int64_t)(token % a.p.page_size) * a.p.row_stride
-                           : 0;
-    const uint32_t dst = ring_u + stage * L::kStage;
+  // this lane's 16 bytes of the first rows that one instruction copies
+  const int64_t lane_off = (lane / CPR) * a.p.row_stride + (lane % CPR) * 16;
+  const uint32_t lane_dst = ring_u + (lane / CPR) * TY::PITCH + (lane % CPR) * 16;
+  int64_t off = 0;      // of this lane's row, or of its bytes where `even`
+  unsigned vis = 0;     // visible tokens of the tile
+  bool even = false;    // all visible, in one page: equal steps from the first row
+  bool values = false;  // what comes next
+  auto load = [&](int slot) {
+    const char *pool = values ? a.p.values : a.p.keys;
+    if (!values) {
+      const bool ok = seen && (unsigned)page < (unsigned)a.p.pages;
+      if (seen && !ok && a.errors && lane < TT) atomicOr(a.errors, (unsigned)FWPKM_CACHE_BAD_PAGE);
+      vis = __ballot_sync(FULL, ok);
+      if (lane == 0) bits[warp][slot] = vis;
+      const int row = token - page_of(a.div, token) * a.p.page_size;
+      const int first = __shfl_sync(FULL, row, 0);
+      off = ok ? page * a.p.page_stride + (int64_t)(ld.hr / a.blocks) * a.p.head_stride +
+                     (int64_t)row * a.p.row_stride
+               : 0;
+      even = vis == FULL && first + TT <= a.p.page_size;
+      if (even) off = __shfl_sync(FULL, off, 0) + lane_off;
+    }
+    if (even) {
+      const char *src = pool + off;
+      const int64_t step = kRows * a.p.row_stride;
+      const uint32_t dst = lane_dst + slot * L::kUnit;
 #pragma unroll
-    for (int i = 0; i < TT * CPR / 32; ++i) {
-      const int flat = i * 32 + lane, row = flat / CPR, c = flat % CPR;
-      const int64_t ro = __shfl_sync(FULL, off, row) + c * 16;
-      const bool rok = (vis >> row) & 1u;
-      if (c < cpr) {
-        cp_async16(dst + row * TY::PITCH + c * 16, rok ? a.p.keys + ro : a.p.keys, rok);
-        cp_async16(dst + L::kTile + row * TY::PITCH + c * 16, rok ? a.p.values + ro : a.p.values,
-                   rok);
+      for (int i = 0; i < kCopies; ++i) {
+        if (lane % CPR + (i % kSteps) * 32 < cpr)
+          cp_async16(dst + (i / kSteps) * kRows * TY::PITCH + (i % kSteps) * 512,
+                     src + (i % kSteps) * 512);
+        if (i % kSteps == kSteps - 1) src += step;
+      }
+    } else {
+      const uint32_t dst = ring_u + slot * L::kUnit;
+#pragma unroll 2
+      for (int i = 0; i < kCopies; ++i) {
+        const int flat = i * 32 + lane, row = flat / CPR, c = flat % CPR;
+        const int64_t ro = __shfl_sync(FULL, off, row) + c * 16;
+        const bool ok = (vis >> row) & 1u;
+        if (c < cpr) cp_async16(dst + row * TY::PITCH + c * 16, ok ? pool + ro : pool, ok);
       }
     }
   };
-  long long next = t0;  // next tile to load
-  if (t0 < t1) look();
-  auto advance = [&](int stage) {
-    if (next < t1) {
-      load(stage);
-      if (++next < t1) {
-        ld.next(a, TT);
-        look();
+  if (ld_unit < u1) look();
+  auto advance = [&](int slot) {
+    if (ld_unit < u1) {
+      load(slot);
+      if (values) {
+        ld_unit += ld.next(lengths, TT);
+        if (ld_unit < u1) look();
       }
+      values = !values;
     }
     cp_commit();
   };
-  for (int i = 0; i < STAGES - 1; ++i) advance(i);
+#pragma unroll 1
+  for (int i = 0; i < UNITS - 1; ++i) advance(i);
 
   // ---- the pass --------------------------------------------------------------
   TY ty;
-  float o[DP / 8][4];
-  float m[2], l[2], c = 0.f;  // of rows g and g + 8; c: scale of the scores
+  ty.reset();
   int rows = 0;
   bool fresh = true, whole = at.tile == 0;
-  auto reset = [&] {
-#pragma unroll
-    for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    m[0] = m[1] = kNegInf;
-    l[0] = l[1] = 0.f;
-  };
-  reset();
-  auto sum_l = [&] {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(FULL, l[r], 1);
-      l[r] += __shfl_xor_sync(FULL, l[r], 2);
-    }
-  };
-  // Row r of the segment's result, finished.
-  auto row_of = [&](const Cursor &k, int r) {
-    return (int64_t)k.b * a.heads + (k.hr / a.blocks) * a.group + (k.hr % a.blocks) * kAttendRows +
-           r;
-  };
-  auto finish = [&] {
-    const float vs = a.p.value_scale ? __ldg(a.p.value_scale + at.hr / a.blocks) : 1.f;
-    float inv[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) inv[r] = l[r] == 0.f ? 0.f : vs / l[r];
-    const int64_t r0 = row_of(at, 0);
-    TY::each(o, [&](int h, int col, float x, float y) {
-      if (g + h * 8 < rows && col < a.p.dim)
-        store2<TO>(a.out + ((r0 + g + h * 8) * a.p.dim + col) * (int64_t)sizeof(TO), x * inv[h],
-                   y * inv[h]);
-    });
-    if (a.lse && (lane & 3) == 0) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (g + h * 8 < rows)
-          a.lse[r0 + g + h * 8] = l[h] == 0.f ? kNegInf : kLn2 * (m[h] + log2f(l[h]));
-    }
-  };
+  long long seg = unit - tile_unit(at.tile);
   auto park = [&](int slot) {
-    float *dst = a.parts + (int64_t)slot * kAttendRows * DP;
-    TY::each(o, [&](int h, int col, float x, float y) {
-      if (g + h * 8 < rows)
-        *reinterpret_cast<float2 *>(dst + (g + h * 8) * DP + col) = make_float2(x, y);
-    });
-    if ((lane & 3) == 0) {
-      a.ml[slot * kAttendRows + g] = make_float2(m[0], l[0]);
-      a.ml[slot * kAttendRows + g + 8] = make_float2(m[1], l[1]);
-    }
+    ty.total();
+    float4 *dst = reinterpret_cast<float4 *>(a.parts + (int64_t)slot * L::kPart) + lane;
+#pragma unroll
+    for (int i = 0; i < TY::kParts; ++i) dst[i * 32] = ty.part(i);
+    ty.stats([&](int h, float m, float l) { a.ml[slot * HEADS + h] = make_float2(m, l); });
+  };
+  auto first_row = [&](int b, int hr) {
+    return (int64_t)b * a.heads + (hr / a.blocks) * a.group + (hr % a.blocks) * HEADS;
   };
 
   int4 tail = make_int4(0, 0, -1, 0);
-  int stage = 0;
-  for (long long t = t0; t < t1; ++t) {
+  bool open = false;  // a part is left in the registers
+  int slot = 0;
+  bool second = false;  // the tile's values are next
+  while (unit < u1) {
     if (fresh) {
-      const int h = at.hr / a.blocks, first = (at.hr % a.blocks) * kAttendRows;
-      rows = min(kAttendRows, a.group - first);
-      ty.load_q(a.q + at.b * a.q_stride + (int64_t)(h * a.group + first) * a.p.dim * sizeof(TO),
-                rows, a.p.dim, qs);
-      c = a.scale_log2 * (a.p.key_scale ? __ldg(a.p.key_scale + h) : 1.f);
+      const int h = at.hr / a.blocks, first = (at.hr % a.blocks) * HEADS;
+      rows = min(HEADS, a.group - first);
+      ty.load_q(a.q + at.b * a.q_stride + (int64_t)(h * a.group + first) * a.p.dim * sizeof(Out),
+                rows, a.p.dim, a.scale_log2 * (a.p.key_scale ? __ldg(a.p.key_scale + h) : 1.f));
       fresh = false;
     }
-    cp_wait<STAGES - 2>();
-    __syncwarp();  // the tile has landed, and the stage before it is free
-    const int into = stage == 0 ? STAGES - 1 : stage - 1;
-    advance(into);
-
-    const uint32_t ks = ring_u + stage * L::kStage, vs = ks + L::kTile;
-    const unsigned vis = bits[warp][stage];
-    float s[TT / 8][4];
-#pragma unroll
-    for (int n = 0; n < TT / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-    ty.scores(s, ks, qs);
-    constexpr unsigned kAll = TT == 32 ? FULL : (1u << (TT % 32)) - 1u;
-    const unsigned my = vis >> (2 * (lane & 3));
-    float top[2] = {kNegInf, kNegInf};
-#pragma unroll
-    for (int n = 0; n < TT / 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[n][i] *= c;
-        if ((vis & kAll) != kAll && !((my >> (8 * n + (i & 1))) & 1u)) s[n][i] = kNegInf;
-        top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
-      }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 1));
-      top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 2));
-      // weights are 2^(s - m); kShift makes the largest 2^kShift
-      top[r] = fmaxf(m[r], top[r] - TY::kShift);
-    }
-    if (__any_sync(FULL, top[0] > m[0] || top[1] > m[1])) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float f = exp2f(m[r] - (top[r] == kNegInf ? 0.f : top[r]));
-        l[r] *= f;
-        m[r] = top[r];
-#pragma unroll
-        for (int n = 0; n < DP / 8; ++n) {
-          o[n][2 * r] *= f;
-          o[n][2 * r + 1] *= f;
+    cp_wait<UNITS - 2>();
+    __syncwarp();  // the unit has landed, and the one before it is free
+    advance(slot == 0 ? UNITS - 1 : slot - 1);
+    const uint32_t src = ring_u + slot * L::kUnit;
+    if (!second) {
+      ty.scores(src, bits[warp][slot]);
+    } else {
+      ty.outputs(src);
+      const bool end = at.tile + 1 == at.s.count;
+      const int b = at.b, hr = at.hr;
+      const int count = at.s.count;
+      unit += at.next(lengths, TT);
+      open = true;
+      if (end) {
+        if (whole) {
+          const int64_t r = first_row(b, hr);
+          ty.finish(reinterpret_cast<Out *>(a.out) + r * a.p.dim, a.lse ? a.lse + r : nullptr,
+                    rows, a.p.dim, a.p.value_scale ? __ldg(a.p.value_scale + hr / a.blocks) : 1.f);
+          open = false;
+        } else if (unit < u1) {
+          park(2 * w);
+          open = false;
+        }
+        if (unit < u1) {
+          ty.reset();
+          fresh = whole = true;
+          seg = unit;
         }
       }
-    }
-    const float u0 = m[0] == kNegInf ? 0.f : m[0], u1 = m[1] == kNegInf ? 0.f : m[1];
-#pragma unroll
-    for (int n = 0; n < TT / 8; ++n) {
-      s[n][0] = exp2f(s[n][0] - u0);
-      s[n][1] = exp2f(s[n][1] - u0);
-      s[n][2] = exp2f(s[n][2] - u1);
-      s[n][3] = exp2f(s[n][3] - u1);
-      l[0] += s[n][0] + s[n][1];
-      l[1] += s[n][2] + s[n][3];
-    }
-    ty.outputs(o, s, vs);
-
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
-    if (at.tile + 1 == at.s.count) {  // the segment ends here
-      if (!joined) {
-        sum_l();
-        if (whole) finish();
-        else park(2 * w);
-        reset();
+      if (unit >= u1 && open) {  // what is left is joined with the CTA's other warps'
+        const int last = line_owner(line, seg + tile_unit(count - 1));
+        if (lane == 0) last_at[warp] = make_int4(b, hr, last, whole);
+        if (whole && !end) tail = make_int4(b, hr, last, 0);
       }
-      fresh = whole = true;
-      if (t + 1 < t1) {
-        at.next(a, TT);
-        seg = t + 1;
-      }
-    } else if (t + 1 < t1) {
-      ++at.tile;
-    } else if (!joined) {  // the segment goes on in the next warp
-      sum_l();
-      park(whole ? 2 * w + 1 : 2 * w);
-      if (whole)
-        tail = make_int4(at.b, at.hr, cache_last_warp(total, warps, seg + at.s.count), 0);
     }
+    second = !second;
+    slot = slot + 1 == UNITS ? 0 : slot + 1;
   }
 
-  // ---- a CTA inside one segment: its warps' sums in one ----------------------
-  const bool all = __syncthreads_or(t0 < t1 && joined);
-  if (all) {
-    sum_l();
-    float *mine = reinterpret_cast<float *>(ring);
-    TY::each(o, [&](int h, int col, float x, float y) {
-      *reinterpret_cast<float2 *>(mine + (g + h * 8) * L::kJoinPitch + col) = make_float2(x, y);
-    });
-    if ((lane & 3) == 0) {
-      jml[warp][g] = make_float2(m[0], l[0]);
-      jml[warp][g + 8] = make_float2(m[1], l[1]);
-    }
-    // warp 0 of such a CTA has tiles: its cursor names the segment
-    __shared__ int4 sseg;
-    __shared__ int srows;
-    if (threadIdx.x == 0) {
-      sseg = make_int4(at.b, at.hr, 0, 0);
-      srows = rows;
-      const bool starts = seg == cta0, ends = seg + at.s.count == cta1;
-      sseg.z = starts && ends ? 1 : 0;
-      sseg.w = starts ? 2 * wa + 1 : 2 * wa;
-      if (starts && !ends)
-        tail = make_int4(at.b, at.hr, cache_last_warp(total, warps, seg + at.s.count), 0);
-    }
-    __syncthreads();
-    const int4 sg = sseg;
-    const int h = sg.y / a.blocks;
-    const float vs = a.p.value_scale ? __ldg(a.p.value_scale + h) : 1.f;
-    const int64_t r0 =
-        (int64_t)sg.x * a.heads + h * a.group + (sg.y % a.blocks) * (int64_t)kAttendRows;
-    for (int i = threadIdx.x; i < srows * (DP / 2); i += WARPS * 32) {
-      const int row = i / (DP / 2), col = (i - row * (DP / 2)) * 2;
-      float top = kNegInf;
+  // ---- the warps' last parts, joined where they are of one segment -------------
+  if (lane == 0) last_seg[warp] = open ? seg : -1;
+  if (open) {
+    ty.total();
+    float4 *mine = reinterpret_cast<float4 *>(ring) + lane;
 #pragma unroll
-      for (int k = 0; k < WARPS; ++k) top = fmaxf(top, jml[k][row].x);
-      const float u = top == kNegInf ? 0.f : top;
-      float x = 0.f, y = 0.f, sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        const float f = exp2f(jml[k][row].x - u);
-        const float2 v = *reinterpret_cast<const float2 *>(
-            smem + k * L::kWarp + (row * L::kJoinPitch + col) * 4);
-        sum = fmaf(jml[k][row].y, f, sum);
-        x = fmaf(v.x, f, x);
-        y = fmaf(v.y, f, y);
-      }
-      if (sg.z) {
-        const float inv = sum == 0.f ? 0.f : vs / sum;
-        if (col < a.p.dim)
-          store2<TO>(a.out + ((r0 + row) * a.p.dim + col) * (int64_t)sizeof(TO), x * inv, y * inv);
-        if (col == 0 && a.lse) a.lse[r0 + row] = sum == 0.f ? kNegInf : kLn2 * (top + log2f(sum));
-      } else {
-        *reinterpret_cast<float2 *>(a.parts + ((int64_t)sg.w * kAttendRows + row) * DP + col) =
-            make_float2(x, y);
-        if (col == 0) a.ml[sg.w * kAttendRows + row] = make_float2(top, sum);
-      }
-    }
-    // the other warps' slots hold nothing
-    if (warp > 0 && lane < kAttendRows && w < warps)
-      a.ml[2 * w * kAttendRows + lane] = make_float2(kNegInf, 0.f);
+    for (int i = 0; i < TY::kParts; ++i) mine[i * 32] = ty.part(i);
+    ty.stats([&](int h, float m, float l) { last_ml[warp][h] = make_float2(m, l); });
   }
-  if (lane == 0) a.tails[w] = tail;
+  if (lane == 0 && warp < per) a.tails[w] = tail;
+  if (threadIdx.x == 0) a.per[blockIdx.x] = per;
+  if (!__syncthreads_or(open)) return;
+  // A run is the neighbouring warps whose last parts are of one segment; its
+  // first warp's slot takes its sum.  Bit k of `heads`: warp k begins a run.
+  // A run that begins its segment takes in what the warp behind it has parked of
+  // that segment, which is then done.
+  const long long my_seg = lane < WARPS ? last_seg[lane] : -1;
+  const long long left = __shfl_up_sync(FULL, my_seg, 1);
+  const unsigned live = __ballot_sync(FULL, my_seg >= 0);
+  const unsigned heads = __ballot_sync(FULL, my_seg >= 0 && (lane == 0 || left != my_seg));
+  if (warp == 0 && (heads >> lane) & 1u) run_at[__popc(heads & lanemask_lt())] = lane;
+  auto run_end = [&](int k0) {  // behind the run that begins at warp k0
+    const unsigned stop = (~live | heads) & (0xfffffffeu << k0);
+    return min(__ffs(stop | 1u << WARPS) - 1, WARPS);
+  };
+  for (int i = threadIdx.x; i < WARPS * HEADS; i += WARPS * 32) {
+    const int k0 = i / HEADS, h = i % HEADS;
+    if (!((heads >> k0) & 1u)) continue;
+    const int k1 = run_end(k0);
+    const int4 id = last_at[k0];
+    const bool more = id.w && id.z == w0 + k1 && k1 < per;
+    float2 end = make_float2(kNegInf, 0.f);
+    if (more) end = a.ml[2 * id.z * HEADS + h];
+    float top = end.x, l = 0.f;
+    for (int k = k0; k < k1; ++k) top = fmaxf(top, last_ml[k][h].x);
+    const float u = top == kNegInf ? 0.f : top;
+    for (int k = k0; k < k1; ++k) {
+      const float2 ml = last_ml[k][h];
+      const float f = ex2(ml.x - u);
+      weight[k][h] = f;
+      l = fmaf(ml.y, f, l);
+    }
+    const float f = ex2(end.x - u);
+    l = fmaf(end.y, f, l);
+    run_ml[k0][h] = make_float2(top, l);
+    end_weight[k0][h] = more ? f : 0.f;
+  }
+  __syncthreads();
+  const int runs = __popc(heads);
+  for (int p = threadIdx.x; p < runs * TY::kParts * 32; p += WARPS * 32) {
+    const int k0 = run_at[p / (TY::kParts * 32)];
+    const int q = p % (TY::kParts * 32), i = q >> 5, ln = q & 31;
+    const int k1 = run_end(k0);
+    const int4 id = last_at[k0];
+    const bool begins = id.w, more = begins && id.z == w0 + k1 && k1 < per;
+    const bool done = begins && (more || id.z < w0 + k1);
+    const int h0 = id.y / a.blocks, block = id.y % a.blocks;
+    const int n = min(HEADS, a.group - block * HEADS);
+    const int to = 2 * (w0 + k0) + (begins ? 1 : 0);
+    int h[4];
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = TY::head_of(i, ln, e);
+    float4 end;
+    if (more) end = reinterpret_cast<const float4 *>(a.parts + (int64_t)(2 * id.z) * L::kPart)[q];
+#pragma unroll 4
+    for (int k = k0; k < k1; ++k) {
+      const float4 v = reinterpret_cast<const float4 *>(smem + k * L::kRing)[q];
+      x[0] = fmaf(v.x, weight[k][h[0]], x[0]);
+      x[1] = fmaf(v.y, weight[k][h[1]], x[1]);
+      x[2] = fmaf(v.z, weight[k][h[2]], x[2]);
+      x[3] = fmaf(v.w, weight[k][h[3]], x[3]);
+    }
+    if (more) {
+      x[0] = fmaf(end.x, end_weight[k0][h[0]], x[0]);
+      x[1] = fmaf(end.y, end_weight[k0][h[1]], x[1]);
+      x[2] = fmaf(end.z, end_weight[k0][h[2]], x[2]);
+      x[3] = fmaf(end.w, end_weight[k0][h[3]], x[3]);
+    }
+    if (done) {
+      const int64_t r = first_row(id.x, id.y);
+      const float vs = a.p.value_scale ? __ldg(a.p.value_scale + h0) : 1.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = TY::col_of(i, ln, e);
+        const float2 ml = run_ml[k0][h[e]];
+        if (h[e] < n && c < a.p.dim)
+          reinterpret_cast<Out *>(a.out)[(r + h[e]) * a.p.dim + c] =
+              to_out<Out>(ml.y == 0.f ? 0.f : x[e] * (vs / ml.y));
+        if (a.lse && h[e] < n && c == 0) a.lse[r + h[e]] = log_sum(ml.x, ml.y);
+      }
+      if (q == 0) a.tails[w0 + k0].z = -1;
+    } else {
+      reinterpret_cast<float4 *>(a.parts + (int64_t)to * L::kPart)[q] =
+          make_float4(x[0], x[1], x[2], x[3]);
+      if (q < HEADS) {
+        a.ml[to * HEADS + q] = run_ml[k0][q];
+        // the slot that k_join may look for at the run's last warp holds nothing
+        if (k1 - k0 > 1) a.ml[2 * (w0 + k1 - 1) * HEADS + q] = make_float2(kNegInf, 0.f);
+      }
+    }
+  }
 }
 
-// Joins the parts of the segments that begin in one CTA's warps: a warp to a
-// query row, two passes over the parts (their maximum, then their sums).
-template <typename TO, int DP, int WARPS>
-__global__ void __launch_bounds__(256) k_join(const __grid_constant__ AttendArgs a) {
+// Joins the parts of segments that lie in more than one slot.  The CTAs whose
+// warps have a part share a segment's groups of 32 x 4 floats out; a group with
+// few parts is one warp's, one with many is summed by all warps of the CTA.
+constexpr int kJoinWarps = 16, kJoinFew = 6;
+template <typename TY>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_join(const __grid_constant__ AttendArgs a) {
+  using Out = typename TY::Out;
+  constexpr int HEADS = TY::HEADS, kPart = TY::kParts * 128;
+  __shared__ float sum[kJoinWarps][12][32];  // of each warp and lane: m, l and x of 4 floats
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
   griddep_launch();
-  constexpr int V = DP / 32;  // columns of a lane, 2 (DP = 64), 4 or 8
-  for (int i = warp; i < WARPS * kAttendRows; i += 8) {
-    const int w = blockIdx.x * WARPS + i / kAttendRows, row = i % kAttendRows;
-    const int4 t = a.tails[w];
-    if (t.z < 0) continue;
-    const int h = t.y / a.blocks, first = (t.y % a.blocks) * kAttendRows;
-    if (row >= a.group - first) continue;
-    const int n = t.z - w + 1;  // parts
-    auto slot = [&](int k) { return k == 0 ? 2 * w + 1 : 2 * (w + k); };
-    float top = kNegInf;
-    for (int k = lane; k < n; k += 32) top = fmaxf(top, a.ml[slot(k) * kAttendRows + row].x);
-    top = warp_max(top);
-    const float u = top == kNegInf ? 0.f : top;
-    float acc[V] = {}, sum = 0.f;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      float f = 0.f;
-      if (k0 + lane < n) {
-        const float2 ml = a.ml[slot(k0 + lane) * kAttendRows + row];
-        f = exp2f(ml.x - u);
-        sum += ml.y * f;
-      }
-      const int most = min(32, n - k0);
-#pragma unroll 4
-      for (int k = 0; k < most; ++k) {
-        const float fk = __shfl_sync(FULL, f, k);
-        if (fk == 0.f) continue;  // an empty slot's sums are not set
-        const float *src =
-            a.parts + ((int64_t)slot(k0 + k) * kAttendRows + row) * DP + lane * V;
+  const int cta = blockIdx.x, per = a.per[cta], w0 = cta * per;
+  // lane i: the segment that begins in warp i; lane 31: the one that goes on here
+  int4 mine = make_int4(0, 0, -1, 0);
+  if (lane < per) {
+    mine = a.tails[w0 + lane];
+    mine.w = w0 + lane;
+  } else if (lane == 31) {
+    mine = a.middles[cta];
+  }
+  unsigned left = __ballot_sync(FULL, mine.z >= 0);
+  int turn = 0;  // single-warp groups dealt out so far
+  for (; left; left &= left - 1) {
+    const int from = __ffs(left) - 1;
+    const int b = __shfl_sync(FULL, mine.x, from), hr = __shfl_sync(FULL, mine.y, from);
+    const int last = __shfl_sync(FULL, mine.z, from), w = __shfl_sync(FULL, mine.w, from);
+    const int c0 = w / per, c1 = last / per;
+    // parts: the first warp's; the first warp's of each later CTA; the last warp's
+    const int n = 1 + c1 - c0 + (last % per != 0);
+    const int h0 = hr / a.blocks, block = hr % a.blocks;
+    const int rows = min(HEADS, a.group - block * HEADS);
+    const int64_t r = (int64_t)b * a.heads + h0 * a.group + block * HEADS;
+    const float vs = a.p.value_scale ? __ldg(a.p.value_scale + h0) : 1.f;
+    const bool many = n > kJoinFew;
+    for (int i = cta - c0; i < TY::kParts; i += c1 - c0 + 1) {
+      if (!many && turn++ % kJoinWarps != warp) continue;
+      int h[4];
+      float top[4], x[4] = {0.f, 0.f, 0.f, 0.f}, l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-          const float2 v = *reinterpret_cast<const float2 *>(src + e);
-          acc[e] = fmaf(v.x, fk, acc[e]);
-          acc[e + 1] = fmaf(v.y, fk, acc[e + 1]);
+      for (int e = 0; e < 4; ++e) {
+        h[e] = TY::head_of(i, lane, e);
+        top[e] = kNegInf;
+      }
+      const int dk = many ? kJoinWarps : 1;
+      for (int kb = many ? warp : 0; kb < n; kb += 4 * dk) {  // four parts at a time
+        float2 ml[4][4];
+        float4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = kb + j * dk;
+          if (k < n) {
+            const int slot = k == 0 ? 2 * w + 1 : k <= c1 - c0 ? 2 * (c0 + k) * per : 2 * last;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ml[j][e] = a.ml[slot * HEADS + h[e]];
+            v[j] = reinterpret_cast<const float4 *>(a.parts + (int64_t)slot * kPart)[i * 32 + lane];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ml[j][e] = make_float2(kNegInf, 0.f);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float t = top[e];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t = fmaxf(t, ml[j][e].x);
+          const float u = t == kNegInf ? 0.f : t, f = ex2(top[e] - u);
+          top[e] = t;
+          l[e] *= f;
+          x[e] *= f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float g = ex2(ml[j][e].x - u);
+            l[e] = fmaf(ml[j][e].y, g, l[e]);
+            // an empty slot's sums are not set
+            if (ml[j][e].y != 0.f)
+              x[e] = fmaf(e == 0 ? v[j].x : e == 1 ? v[j].y : e == 2 ? v[j].z : v[j].w, g, x[e]);
+          }
         }
       }
-    }
-    sum = warp_sum(sum);
-    const float vs = a.p.value_scale ? __ldg(a.p.value_scale + h) : 1.f;
-    const float inv = sum == 0.f ? 0.f : vs / sum;
-    const int64_t r = (int64_t)t.x * a.heads + h * a.group + first + row;
+      if (many) {
 #pragma unroll
-    for (int e = 0; e < V; e += 2)
-      if (lane * V + e < a.p.dim)
-        store2<TO>(a.out + (r * a.p.dim + lane * V + e) * (int64_t)sizeof(TO), acc[e] * inv,
-                   acc[e + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[r] = sum == 0.f ? kNegInf : kLn2 * (top + log2f(sum));
+        for (int e = 0; e < 4; ++e) {
+          sum[warp][e][lane] = top[e];
+          sum[warp][4 + e][lane] = l[e];
+          sum[warp][8 + e][lane] = x[e];
+        }
+        __syncthreads();
+        if (warp < 4) {  // warp e: float e
+          const int e = warp;
+          float t = kNegInf, xe = 0.f, le = 0.f;
+#pragma unroll
+          for (int k = 0; k < kJoinWarps; ++k) t = fmaxf(t, sum[k][e][lane]);
+          const float u = t == kNegInf ? 0.f : t;
+#pragma unroll
+          for (int k = 0; k < kJoinWarps; ++k) {
+            const float f = ex2(sum[k][e][lane] - u);
+            le = fmaf(sum[k][4 + e][lane], f, le);
+            xe = fmaf(sum[k][8 + e][lane], f, xe);
+          }
+          const int he = TY::head_of(i, lane, e), c = TY::col_of(i, lane, e);
+          if (he < rows) {
+            if (c < a.p.dim)
+              reinterpret_cast<Out *>(a.out)[(r + he) * a.p.dim + c] =
+                  to_out<Out>(le == 0.f ? 0.f : xe * (vs / le));
+            if (a.lse && c == 0) a.lse[r + he] = log_sum(t, le);
+          }
+        }
+        __syncthreads();
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = TY::col_of(i, lane, e);
+        if (h[e] >= rows) continue;
+        if (c < a.p.dim)
+          reinterpret_cast<Out *>(a.out)[(r + h[e]) * a.p.dim + c] =
+              to_out<Out>(l[e] == 0.f ? 0.f : x[e] * (vs / l[e]));
+        if (a.lse && c == 0) a.lse[r + h[e]] = log_sum(top[e], l[e]);
+      }
+    }
   }
 }
 
-template <typename TY, typename TO, int WARPS, int STAGES>
-cudaError_t launch(const AttendArgs &a, cudaStream_t st) {
-  using L = Layout<TY, WARPS, STAGES>;
-  auto *kernel = k_attend<TY, TO, WARPS, STAGES>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+// Attributes of the kernels, set once a device.  k_join asks for the shared
+// memory split that k_attend runs with: a multiprocessor changes its split only
+// when it is idle, which would keep the join from starting early.
+template <typename TY, int WARPS, int UNITS>
+cudaError_t prepare() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = launch_k(true, kernel, dim3(kAttendCtas), dim3(WARPS * 32), L::kSmem, st, a);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(k_attend<TY, WARPS, UNITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Layout<TY, WARPS, UNITS>::kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_attend<TY, WARPS, UNITS>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_join<TY>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <typename TY, int WARPS, int UNITS>
+cudaError_t launch(AttendArgs a, cudaStream_t st) {
+  cudaError_t e = prepare<TY, WARPS, UNITS>();
   if (e != cudaSuccess) return e;
-  return launch_k(true, k_join<TO, TY::DP, WARPS>, dim3(kAttendCtas), dim3(256), 0, st, a);
+  const AttendShape s = attend_shape(TY::kDtype, a.p.dim, a.group);
+  if (s.warps != WARPS || s.heads != TY::HEADS || s.part != TY::kParts * 128)
+    return cudaErrorInvalidConfiguration;  // the workspace has another layout
+  a.blocks = (a.group + TY::HEADS - 1) / TY::HEADS;
+  e = launch_k(true, k_attend<TY, WARPS, UNITS>, dim3(kAttendCtas), dim3(WARPS * 32),
+               Layout<TY, WARPS, UNITS>::kSmem, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_k(true, k_join<TY>, dim3(kAttendCtas), dim3(kJoinWarps * 32), 0,
+                  st, a);
 }
 
 }  // namespace attend

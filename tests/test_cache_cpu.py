@@ -28,9 +28,14 @@ void span(int len, int window, int tile, int *o) {
   Span s = cache_span(len, window, tile);
   o[0] = s.lo; o[1] = s.len; o[2] = s.first; o[3] = s.count;
 }
-int warps(int64_t total, int most, int least) { return cache_warps(total, most, least); }
-int64_t cut(int64_t total, int n, int w) { return cache_cut(total, n, w); }
-int last(int64_t total, int n, int64_t end) { return cache_last_warp(total, n, end); }
+int warps(int64_t total, int most) { return cache_line(total, most).warps; }
+int64_t cut(int64_t total, int most, int w) { return line_cut(cache_line(total, most), w); }
+int owner(int64_t total, int most, int64_t unit) { return line_owner(cache_line(total, most), unit); }
+int per_cta(int64_t total, int most, int ctas) { return line_per_cta(cache_line(total, most), ctas); }
+int64_t units(int tiles) { return segment_units(tiles); }
+int64_t unit_of(int j) { return tile_unit(j); }
+int from(int64_t u) { return tile_from(u); }
+int page(int d, int t) { return page_of(page_div(d), t); }
 int length(int len, int width, int page, int *bad) {
   bool b; int r = cache_length(len, width, page, b); *bad = b; return r;
 }
@@ -50,8 +55,11 @@ def sched(tmp_path_factory):
                     "-static-libubsan", "-shared", "-fPIC", "-I", fwbuild.CSRC,
                     str(d / "shim.cpp"), "-o", so], check=True)
     L = ctypes.CDLL(so)
-    L.warps.argtypes, L.cut.argtypes = [i64, i32, i32], [i64, i32, i32]
-    L.cut.restype, L.last.argtypes = i64, [i64, i32, i64]
+    L.warps.argtypes, L.cut.argtypes = [i64, i32], [i64, i32, i32]
+    L.per_cta.argtypes = [i64, i32, i32]
+    L.owner.argtypes, L.from_ = [i64, i32, i64], getattr(L, "from")
+    L.from_.argtypes = [i64]
+    L.cut.restype = L.units.restype = L.unit_of.restype = i64
     return L
 
 
@@ -76,28 +84,56 @@ def test_span_covers_the_visible_tokens(sched, tile, window):
             assert (first + count - 1) * tile < n <= (first + count) * tile
 
 
-def test_pieces_tile_the_line_and_parts_are_listed(sched):
-    """Every tile is in one warp's piece, pieces differ by one tile at most, and
-    the last warp of a segment is the one that holds its last tile."""
+def test_pieces_share_the_line_out(sched):
+    """Every tile of every segment belongs to one warp; pieces differ by a unit at
+    most; and a segment's parts are those of its first warp to its last, none
+    of them without a tile."""
     rng = np.random.default_rng(0)
-    for _ in range(300):
-        total = int(np.exp(rng.uniform(0, np.log(1e6))))
-        n = sched.warps(total, int(rng.choice([592, 1184])), 2)
-        assert 1 <= n <= 1184 and (n == 1 or total >= 2 * n)
-        cuts = [sched.cut(total, n, w) for w in range(n + 1)]
+    for round_ in range(150):
+        most = int(rng.choice([1, 5, 592, 1184, 2368]))
+        big = int(np.exp(rng.uniform(0, np.log(3000))))
+        counts = [int(c) for c in rng.integers(1, big + 1, int(rng.integers(1, 60)))]
+        at = np.cumsum([0] + [sched.units(c) for c in counts])
+        total = int(at[-1])
+        n = sched.warps(total, most)
+        cuts = [sched.cut(total, most, w) for w in range(n + 1)]
         sizes = np.diff(cuts)
-        assert cuts[0] == 0 and cuts[-1] == total and sizes.min() >= 1
-        assert sizes.max() - sizes.min() <= 1
-        for end in {1, total, *(int(x) for x in rng.integers(1, total + 1, 20)), *cuts[1:5]}:
-            w = sched.last(total, n, end)
-            assert cuts[w] < end <= cuts[w + 1]
+        assert 1 <= n <= most and cuts[0] == 0 and cuts[-1] == total
+        assert sizes.max() - sizes.min() <= 1 and (n == 1 or sizes.min() >= 4)
+        ctas = -(-most // 16)
+        per = sched.per_cta(total, most, ctas)
+        assert per * ctas >= n and per <= max(4, -(-most // ctas))
+        for c, first in zip(counts, at[:-1]):
+            unit = [int(first) + sched.unit_of(j) for j in range(c)]
+            assert unit[-1] < first + sched.units(c)
+            owner = np.searchsorted(cuts, unit, side="right") - 1
+            for j in {0, c - 1, c // 2}:
+                assert sched.owner(total, most, unit[j]) == owner[j]
+            assert set(owner) == set(range(owner[0], owner[-1] + 1))
+            for w in range(owner[0], owner[-1] + 1):  # where the warp enters the segment
+                j = sched.from_(max(0, cuts[w] - int(first)))
+                assert j == int(np.searchsorted(owner, w))
 
 
 def test_largest_line_stays_within_64_bits(sched):
-    total = (1 << 22) * (1 << 28)  # B * heads times the tiles of 2^31 tokens
-    assert sched.cut(total, 1184, 1184) == total
-    assert sched.last(total, 1184, total) == 1183
-    assert sched.last(total, 1184, 1) == 0
+    total = (1 << 22) * ((1 << 28) + 2)  # B * heads times the units of 2^31 tokens
+    assert sched.cut(total, 2368, 2368) == total
+    assert sched.owner(total, 2368, total - 1) == 2367
+    assert sched.owner(total, 2368, 0) == 0
+
+
+def test_page_of_a_token_is_the_quotient(sched):
+    top = 2**31 - 1
+    rng = np.random.default_rng(1)
+    sizes = [*range(1, 40), 48, 63, 64, 65, 100, 127, 1000, 2**16 + 1, 2**30, 2**30 + 1, top - 1,
+             top, *(int(x) for x in rng.integers(1, top, 50))]
+    for d in sizes:
+        tokens = {0, 1, d - 1, d, top, top - 1, top // d * d, max(0, top // d * d - 1),
+                  *(int(x) for x in rng.integers(0, top, 30)),
+                  *(int(x) * d % (top + 1) for x in rng.integers(0, top, 10))}
+        for t in tokens:
+            if t <= top:
+                assert sched.page(d, t) == t // d
 
 
 def test_lengths_stay_within_the_table(sched):
