@@ -19,7 +19,11 @@ ROTATE = {"halves": 0, "pairs": 1}
 BAD_PAGE, BAD_LENGTH = 32, 64  # bits of an `errors` word
 
 _DTYPES = {torch.float32: FWPKM_F32, torch.bfloat16: FWPKM_BF16, torch.float8_e4m3fn: E4M3}
+_INPUTS = {torch.float32: FWPKM_F32, torch.bfloat16: FWPKM_BF16}
 _vp = ctypes.c_void_p
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _Cache(ctypes.Structure):  # fwpkm_cache
@@ -116,9 +120,11 @@ class KVCache:
         self._c = _Cache(keys.data_ptr(), values.data_ptr(), ps, hs, rs, self.pages,
                          self.page_size, self.kv_heads, self.dim, _DTYPES[self.dtype],
                          *(None if s is None else s.data_ptr() for s in self._scales))
-        self._ref = ctypes.byref(self._c)
+        self._ref, self._lib = self._c, _library()
+        self._scale = 1.0 / math.sqrt(self.dim)
         # what the sizes alone decide is refused here
-        _check(_library().fwpkm_cache_attend_workspace(self._ref, 1, self.kv_heads))
+        self._bytes = {}  # workspace bytes by (B, heads)
+        self.attend_workspace(1, self.kv_heads)
 
     @property
     def keys(self):
@@ -129,6 +135,8 @@ class KVCache:
         return self._values
 
     # -- checks --------------------------------------------------------------
+    # Each call checks every tensor it hands on; the common case is kept short,
+    # since a small call takes less time on the GPU than in here.
     def _on_device(self, t, dtype, name, contiguous=True):
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
@@ -140,27 +148,30 @@ class KVCache:
     def _batch(self, table, lengths):
         self._on_device(table, torch.int32, "table", contiguous=False)
         self._on_device(lengths, torch.int32, "lengths")
-        _shape(table.dim() == 2 and lengths.dim() == 1 and table.shape[0] == lengths.shape[0],
-               "table must be [B][width] and lengths [B]")
-        B, width = table.shape
-        _shape(B >= 1 and width >= 1, "B and the table's width must be >= 1")
-        _shape((width == 1 or table.stride(1) == 1) and (B == 1 or table.stride(0) >= width),
-               "table rows must be contiguous")
-        return _Batch(B, width, table.stride(0) if B > 1 else width, table.data_ptr(),
-                      lengths.data_ptr())
+        shape = table.shape
+        if len(shape) != 2 or lengths.shape != shape[:1] or 0 in shape:
+            raise FwpkmError(FWPKM_ESHAPE, "table must be [B][width] and lengths [B], B and width "
+                             ">= 1")
+        B, width = shape
+        rows, cols = table.stride()
+        if (cols != 1 and width > 1) or (rows < width and B > 1):
+            raise FwpkmError(FWPKM_ESHAPE, "table rows must be contiguous")
+        return _Batch(B, width, rows if B > 1 else width, table.data_ptr(), lengths.data_ptr())
 
-    def _rows(self, t, name, dtype, heads=None):
-        """[rows][heads][dim] with contiguous rows; the stride between rows."""
+    def _rows(self, t, name, dtype, rows, heads=None):
+        """The element stride between the rows of t [rows][heads][dim], each contiguous."""
         self._on_device(t, dtype, name, contiguous=False)
-        _shape(t.dim() == 3 and t.shape[2] == self.dim and (heads is None or t.shape[1] == heads),
-               f"{name} must be [rows][{'heads' if heads is None else heads}][{self.dim}]")
-        _shape(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == self.dim),
-               f"the rows of {name} must be contiguous")
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * self.dim
+        shape = t.shape
+        if len(shape) != 3 or shape[0] != rows or shape[2] != self.dim or \
+                (heads is not None and shape[1] != heads):
+            raise FwpkmError(FWPKM_ESHAPE, f"{name} must be [{rows}]"
+                             f"[{'heads' if heads is None else heads}][{self.dim}]")
+        step, head, one = t.stride()
+        if one != 1 or (head != self.dim and shape[1] > 1):
+            raise FwpkmError(FWPKM_ESHAPE, f"the rows of {name} must be contiguous")
+        return step if rows > 1 else shape[1] * self.dim
 
     def _errors(self, errors):
-        if errors is None:
-            return None
         self._on_device(errors, torch.int32, "errors")
         _shape(errors.numel() >= 1, "errors must hold a word")
         return errors.data_ptr()
@@ -171,7 +182,7 @@ class KVCache:
     def _current_stream(self):
         if self.device.type != "cuda":
             raise FwpkmError(FWPKM_EINVAL, f"the cache is on {self.device}, not on a CUDA device")
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.device.index)
 
     @contextlib.contextmanager
     def _other(self, stream):
@@ -203,38 +214,43 @@ class KVCache:
 
     def _append(self, k, v, table, lengths, starts, q, freqs, style, q_out, errors):
         batch = self._batch(table, lengths)
-        if k.dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"unsupported dtype {k.dtype}")
+        dtype = k.dtype
+        if dtype not in _INPUTS:
+            raise TypeError(f"unsupported dtype {dtype}")
         if style not in ROTATE:
             raise FwpkmError(FWPKM_EINVAL, f"style must be one of {sorted(ROTATE)}")
-        k_stride = self._rows(k, "k", k.dtype, self.kv_heads)
-        v_stride = self._rows(v, "v", k.dtype, self.kv_heads)
-        rows = k.shape[0]
-        _shape(v.shape[0] == rows, "k and v must have the same rows")
-        heads = q_stride = out_stride = 0
+        rows = k.shape[0] if k.dim() else 0
+        k_stride = self._rows(k, "k", dtype, rows, self.kv_heads)
+        v_stride = self._rows(v, "v", dtype, rows, self.kv_heads)
+        heads = q_stride = out_stride = rotary = 0
+        q_at = out_at = starts_at = freqs_at = None
         if q is not None:
-            q_stride, heads = self._rows(q, "q", k.dtype), q.shape[1]
-            _shape(q.shape[0] == rows, "k and q must have the same rows")
+            q_stride = self._rows(q, "q", dtype, rows)
+            heads = q.shape[1]
             if q_out is None:
-                q_out = torch.empty((rows, heads, self.dim), dtype=q.dtype, device=q.device)
-            out_stride = self._rows(q_out, "q_out", q.dtype, heads)
-            _shape(q_out.shape[0] == rows, "q and q_out must have the same rows")
+                q_out = torch.empty((rows, heads, self.dim), dtype=dtype, device=self.device)
+                out_stride = heads * self.dim
+            else:
+                out_stride = self._rows(q_out, "q_out", dtype, rows, heads)
+            q_at, out_at = q.data_ptr(), q_out.data_ptr()
         elif q_out is not None:
             raise FwpkmError(FWPKM_EINVAL, "q_out without q")
-        rotary = 0
         if freqs is not None:
             self._on_device(freqs, torch.float32, "freqs")
             rotary = 2 * freqs.numel()
+            freqs_at = freqs.data_ptr() if rotary else None
         if starts is not None:
             self._on_device(starts, torch.int32, "starts")
             _shape(starts.shape == (batch.B + 1,), "starts must be [B+1]")
-        _check(_library().fwpkm_cache_append(
-            self._ref, ctypes.byref(batch), rows, _DTYPES[k.dtype], k.data_ptr(), k_stride,
-            v.data_ptr(), v_stride, None if q is None else q.data_ptr(), q_stride,
-            None if q is None else q_out.data_ptr(), out_stride, heads,
-            None if starts is None else starts.data_ptr(), rotary, ROTATE[style],
-            freqs.data_ptr() if rotary else None, self._errors(errors),
-            self._current_stream()))
+            starts_at = starts.data_ptr()
+        if errors is not None:
+            errors = self._errors(errors)
+        rc = self._lib.fwpkm_cache_append(
+            self._ref, batch, rows, _INPUTS[dtype], k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+            q_at, q_stride, out_at, out_stride, heads, starts_at, rotary, ROTATE[style], freqs_at,
+            errors, self._current_stream())
+        if rc:
+            _check(rc)
         return q_out
 
     def attend(self, q, table, lengths, scale: Optional[float] = None, window: int = 0, out=None,
@@ -243,7 +259,8 @@ class KVCache:
         cached tokens (the last ``window`` of them, or all): returns ``out``
         [B][heads][dim]; ``lse`` (fp32 [B][heads], optional) receives the log
         of the softmax's denominator.  ``scale`` defaults to 1/sqrt(dim).
-        ``workspace``: see ``attend_workspace``; allocated per call without."""
+        ``workspace`` (uint8, ``attend_workspace`` bytes) is this call's alone
+        until it has run; without one it is allocated per call."""
         if stream is not None or self._elsewhere():
             with self._other(stream):
                 return self._attend(q, table, lengths, scale, window, out, lse, errors, workspace)
@@ -251,31 +268,41 @@ class KVCache:
 
     def _attend(self, q, table, lengths, scale, window, out, lse, errors, workspace):
         batch = self._batch(table, lengths)
-        if q.dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"unsupported dtype {q.dtype}")
-        q_stride = self._rows(q, "q", q.dtype)
-        B, heads, _ = q.shape
-        _shape(B == batch.B, "q must have a row for each sequence")
+        dtype, B = q.dtype, batch.B
+        if dtype not in _INPUTS:
+            raise TypeError(f"unsupported dtype {dtype}")
+        q_stride = self._rows(q, "q", dtype, B)
+        heads = q.shape[1]
+        need = self.attend_workspace(B, heads)
         if out is None:
-            out = torch.empty((B, heads, self.dim), dtype=q.dtype, device=q.device)
+            out = torch.empty((B, heads, self.dim), dtype=dtype, device=self.device)
         else:
-            self._on_device(out, q.dtype, "out")
+            self._on_device(out, dtype, "out")
             _shape(out.shape == q.shape, "out must be [B][heads][dim]")
+        lse_at = None
         if lse is not None:
             self._on_device(lse, torch.float32, "lse")
             _shape(lse.shape == (B, heads), "lse must be [B][heads]")
+            lse_at = lse.data_ptr()
         if workspace is None:
-            workspace = torch.empty(self.attend_workspace(B, heads), dtype=torch.uint8,
-                                    device=q.device)
+            workspace, size = torch.empty(need, dtype=torch.uint8, device=self.device), need
         else:
             self._on_device(workspace, torch.uint8, "workspace")
-        _check(_library().fwpkm_cache_attend(
-            self._ref, ctypes.byref(batch), heads, _DTYPES[q.dtype], q.data_ptr(), q_stride,
-            1.0 / math.sqrt(self.dim) if scale is None else scale, window, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-            self._errors(errors), self._current_stream()))
+            size = workspace.numel()
+        if errors is not None:
+            errors = self._errors(errors)
+        rc = self._lib.fwpkm_cache_attend(
+            self._ref, batch, heads, _INPUTS[dtype], q.data_ptr(), q_stride,
+            self._scale if scale is None else scale, window, out.data_ptr(), lse_at,
+            workspace.data_ptr(), size, errors, self._current_stream())
+        if rc:
+            _check(rc)
         return out
 
     def attend_workspace(self, B: int, heads: int) -> int:
         """Bytes of device memory that one running ``attend`` of these sizes needs."""
-        return _check(_library().fwpkm_cache_attend_workspace(self._ref, B, heads))
+        need = self._bytes.get((B, heads))
+        if need is None:
+            need = _check(self._lib.fwpkm_cache_attend_workspace(self._ref, B, heads))
+            self._bytes[B, heads] = need
+        return need

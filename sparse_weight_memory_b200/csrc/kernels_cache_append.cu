@@ -16,20 +16,39 @@
 namespace fwpkm {
 namespace {
 
-constexpr int kMaxRowsPerCta = 8;
+constexpr int kMaxThreads = 512;
+constexpr int kMaxBlock = 8;     // rows of a block
+constexpr int kMaxChunk = 256;   // rows of a CTA
 constexpr int kMaxPairs = FWPKM_CACHE_MAX_DIM / 2;
 
 struct Eight {
   float x[8];
 };
-__device__ __forceinline__ Eight load8(const float *p) {
-  const float4 a = *reinterpret_cast<const float4 *>(p);
-  const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load8(const T *p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+  return r;
 }
-__device__ __forceinline__ Eight load8(const __nv_bfloat16 *p) {
-  const uint4 raw = *reinterpret_cast<const uint4 *>(p);
-  const unsigned w[4] = {raw.x, raw.y, raw.z, raw.w};
+__device__ __forceinline__ Eight unpack(const Raw<float> &r) {
+  Eight e;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    e.x[4 * i] = __uint_as_float(r.w[i].x);
+    e.x[4 * i + 1] = __uint_as_float(r.w[i].y);
+    e.x[4 * i + 2] = __uint_as_float(r.w[i].z);
+    e.x[4 * i + 3] = __uint_as_float(r.w[i].w);
+  }
+  return e;
+}
+__device__ __forceinline__ Eight unpack(const Raw<__nv_bfloat16> &r) {
+  const unsigned w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
   Eight e;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -64,24 +83,22 @@ struct Place {
   int pos;
 };
 
-// Warp-level: the place of row r.
+// The place of row r.
 __device__ Place find_place(const AppendArgs &a, int r) {
-  const int lane = threadIdx.x & 31;
   Place pl{-1, -1};
   int b = r, after = 1;  // after: rows from r to the sequence's end
   int before = 0;
   if (a.starts) {
     if (r >= __ldg(a.starts + a.s.B)) return pl;
-    // the last b with starts[b] <= r: 32 probes a step
-    int lo = 0, n = a.s.B;  // among starts[lo .. lo + n - 1]
+    int lo = 0, n = a.s.B;  // the last b with starts[b] <= r is among lo .. lo + n - 1
     while (n > 1) {
-      const int step = (n + 31) / 32;
-      const int i = lane * step;
-      const bool le = i < n && __ldg(a.starts + lo + i) <= r;
-      const unsigned hits = __ballot_sync(FULL, le);
-      const int last = hits ? 31 - __clz(hits) : 0;
-      lo += last * step;
-      n = min(step, n - last * step);
+      const int half = n >> 1;
+      if (__ldg(a.starts + lo + half) <= r) {
+        lo += half;
+        n -= half;
+      } else {
+        n = half;
+      }
     }
     b = lo;
     before = r - __ldg(a.starts + b);
@@ -98,7 +115,7 @@ __device__ Place find_place(const AppendArgs &a, int r) {
     else
       pl.off = page * a.p.page_stride + (int64_t)(pl.pos % a.p.page_size) * a.p.row_stride;
   }
-  if (bad && a.errors && lane == 0) atomicOr(a.errors, bad);
+  if (bad && a.errors) atomicOr(a.errors, bad);
   return pl;
 }
 
@@ -107,117 +124,175 @@ __device__ __forceinline__ void divide(Eight &e, float by) {
   for (int i = 0; i < 8; ++i) e.x[i] = __fdiv_rn(e.x[i], by);
 }
 
-// A CTA takes `per_cta` consecutive rows.  Its threads share out the row's
-// items: an item is 8 elements of a head, or, in a head rotated by halves, two
-// groups of 8 that turn together.
-template <typename TI, typename TC>
-__global__ void __launch_bounds__(512) k_append(const __grid_constant__ AppendArgs a, int per_cta) {
-  __shared__ Place place[kMaxRowsPerCta];
-  __shared__ float2 turn[kMaxRowsPerCta * kMaxPairs];  // (cos, sin) of each row's angles
+// What a thread does of a row: 8 elements of a head or, in a head rotated by
+// halves, two groups of 8 that turn together.
+struct Item {
+  bool is_q, is_v;
+  int head, c, c2;  // c: group of 8; c2: its partner, or -1
+};
+__device__ __forceinline__ Item item_of(const AppendArgs &a, int it) {
+  const int D8 = a.p.dim / 8, H8 = a.rotary / 16;
+  const int turned = a.pairs ? D8 : D8 - H8;  // items of a query or key head
+  const int qk = (a.heads + a.p.kv_heads) * turned;
+  Item m;
+  m.is_v = it >= qk;
+  m.is_q = false;
+  m.c2 = -1;
+  if (m.is_v) {
+    m.head = (it - qk) / D8;
+    m.c = (it - qk) - m.head * D8;
+  } else {
+    m.head = it / turned;
+    m.c = it - m.head * turned;
+    m.is_q = m.head < a.heads;  // queries first
+    if (!m.is_q) m.head -= a.heads;
+    if (!a.pairs) {
+      if (m.c < H8) m.c2 = m.c + H8;
+      else m.c += H8;  // behind the rotated elements
+    }
+  }
+  return m;
+}
+int items_of_row(const AppendArgs &a) {
+  const int D8 = a.p.dim / 8, H8 = a.rotary / 16;
+  return (a.heads + a.p.kv_heads) * (a.pairs ? D8 : D8 - H8) + a.p.kv_heads * D8;
+}
+
+// A CTA takes `chunk` consecutive rows in blocks of groups x ROWS, a thread the
+// same items of ROWS rows of a block.  Finding where a row goes takes dependent
+// loads: a thread to a row, all of the CTA's rows at once.  In the loop a
+// block's elements are loaded, all rows' at once, before the next block's angles
+// are computed, so the memory is busy meanwhile.
+template <typename TI, typename TC, int ROWS>
+__global__ void __launch_bounds__(kMaxThreads, 2)
+    k_append(const __grid_constant__ AppendArgs a, int chunk, int per_row, int groups,
+             int per_group) {
+  __shared__ Place place[kMaxChunk];
+  __shared__ float2 turn[2][kMaxBlock * kMaxPairs];  // (cos, sin) of a block's angles
   griddep_wait();
   griddep_launch();
-  const int r0 = blockIdx.x * per_cta;
-  const int nrows = min(per_cta, a.rows - r0);
-  for (int i = threadIdx.x >> 5; i < nrows; i += blockDim.x >> 5) {
-    const Place pl = find_place(a, r0 + i);
-    if ((threadIdx.x & 31) == 0) place[i] = pl;
-  }
+  const int r0 = blockIdx.x * chunk, rows = min(chunk, a.rows - r0);
+  const int block = groups * ROWS, half = a.rotary / 2;
+  const int group = threadIdx.x / per_group, it0 = threadIdx.x - group * per_group;
+  for (int i = threadIdx.x; i < rows; i += blockDim.x) place[i] = find_place(a, r0 + i);
   __syncthreads();
-  const int half = a.rotary / 2;
-  for (int i = threadIdx.x; i < nrows * half; i += blockDim.x) {
-    const int row = i / half, j = i - row * half;
-    // in turns, reduced to [-1/2, 1/2]: 1 / (2 pi) in 64 bits
-    const double t = (double)max(place[row].pos, 0) * (double)__ldg(a.freqs + j) *
-                     0.15915494309189533577;
-    float sn, cs;
-    sincospif(2.f * (float)(t - rint(t)), &sn, &cs);
-    turn[row * half + j] = make_float2(cs, sn);
-  }
-  __syncthreads();
-
-  const int D8 = a.p.dim / 8, R8 = a.rotary / 8, H8 = R8 / 2;
-  const int turned = a.pairs ? D8 : D8 - H8;  // items of a query or key head
-  const int qk = a.heads + a.p.kv_heads;      // of them the first a.heads are queries
-  const int per_row = qk * turned + a.p.kv_heads * D8;
-  for (int i = threadIdx.x; i < nrows * per_row; i += blockDim.x) {
-    const int row = i / per_row;
-    int it = i - row * per_row;
-    const int r = r0 + row;
-    const Place pl = place[row];
-    int head, c;
-    const TI *src;
-    bool is_v = it >= qk * turned, is_q = false;
-    if (is_v) {
-      it -= qk * turned;
-      head = it / D8;
-      c = it - head * D8;
-      src = reinterpret_cast<const TI *>(a.v + r * a.v_stride) + head * a.p.dim;
-    } else {
-      head = it / turned;
-      c = it - head * turned;
-      is_q = head < a.heads;
-      if (!is_q) head -= a.heads;
-      src = reinterpret_cast<const TI *>(is_q ? a.q + r * a.q_stride : a.k + r * a.k_stride) +
-            head * a.p.dim;
+  auto angles = [&](int b0) {
+    const int n = min(block, rows - b0) * half;
+    float2 *to = turn[b0 / block & 1];
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const int row = i / half, j = i - row * half;
+      // in turns, reduced to [-1/2, 1/2]: 1 / (2 pi) in 64 bits
+      const double t = (double)max(place[b0 + row].pos, 0) * (double)__ldg(a.freqs + j) *
+                       0.15915494309189533577;
+      float sn, cs;
+      sincospif(2.f * (float)(t - rint(t)), &sn, &cs);
+      to[i] = make_float2(cs, sn);
     }
-    if (is_q ? pl.pos < 0 : pl.off < 0) continue;
-    int c2 = -1;  // the partner group of 8, in a head rotated by halves
-    if (!is_v && !a.pairs) {
-      if (c < H8) c2 = c + H8;
-      else c += H8;  // behind the rotated elements
-    }
-    Eight x = load8(src + c * 8), y;
-    if (c2 >= 0) {
-      y = load8(src + c2 * 8);
-      const float2 *t = turn + row * half + c * 8;
+  };
+  angles(0);
+  for (int b0 = 0; b0 < rows; b0 += block) {
+    const float2 *at = turn[b0 / block & 1];
+    bool first = true;
+    for (int it = it0;; it += per_group) {
+      const bool live = group < groups && it < per_row;
+      Item m{};
+      Raw<TI> x[ROWS], y[ROWS];
+      if (live) {
+        m = item_of(a, it);
+        const char *base = m.is_v ? a.v : m.is_q ? a.q : a.k;
+        const int64_t stride = m.is_v ? a.v_stride : m.is_q ? a.q_stride : a.k_stride;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 w = t[e];
-        const float u = x.x[e], z = y.x[e];
-        x.x[e] = u * w.x - z * w.y;
-        y.x[e] = z * w.x + u * w.y;
+        for (int j = 0; j < ROWS; ++j) {
+          const int row = b0 + group + j * groups;
+          if (row >= rows) continue;
+          const TI *src =
+              reinterpret_cast<const TI *>(base + (r0 + row) * stride) + m.head * a.p.dim;
+          x[j] = load8(src + m.c * 8);
+          if (m.c2 >= 0) y[j] = load8(src + m.c2 * 8);
+        }
       }
-    } else if (!is_v && a.pairs && c < R8) {
-      const float2 *t = turn + row * half + c * 4;
+      if (first) {
+        __syncthreads();  // this block's angles are there, the last block's are used
+        if (b0 + block < rows) angles(b0 + block);
+        first = false;
+      }
+      if (!live) break;
+      const float *scale = m.is_q ? nullptr : m.is_v ? a.p.value_scale : a.p.key_scale;
+      const float by = scale ? __ldg(scale + m.head) : 1.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 w = t[e];
-        const float u = x.x[2 * e], z = x.x[2 * e + 1];
-        x.x[2 * e] = u * w.x - z * w.y;
-        x.x[2 * e + 1] = z * w.x + u * w.y;
+      for (int j = 0; j < ROWS; ++j) {
+        const int row = group + j * groups;
+        if (b0 + row >= rows) continue;
+        const Place pl = place[b0 + row];
+        if (m.is_q ? pl.pos < 0 : pl.off < 0) continue;
+        Eight u = unpack(x[j]), z;
+        if (m.c2 >= 0) {
+          z = unpack(y[j]);
+          const float4 *t = reinterpret_cast<const float4 *>(at + row * half + m.c * 8);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float4 w = t[e / 2];
+            const float u0 = u.x[e], z0 = z.x[e], u1 = u.x[e + 1], z1 = z.x[e + 1];
+            u.x[e] = u0 * w.x - z0 * w.y;
+            z.x[e] = z0 * w.x + u0 * w.y;
+            u.x[e + 1] = u1 * w.z - z1 * w.w;
+            z.x[e + 1] = z1 * w.z + u1 * w.w;
+          }
+        } else if (!m.is_v && a.pairs && m.c < a.rotary / 8) {
+          const float2 *t = at + row * half + m.c * 4;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 w = t[e];
+            const float u0 = u.x[2 * e], z0 = u.x[2 * e + 1];
+            u.x[2 * e] = u0 * w.x - z0 * w.y;
+            u.x[2 * e + 1] = z0 * w.x + u0 * w.y;
+          }
+        }
+        if (m.is_q) {
+          TI *dst = reinterpret_cast<TI *>(a.q_out + (r0 + b0 + row) * a.q_out_stride) +
+                    m.head * a.p.dim;
+          store8(dst + m.c * 8, u);
+          if (m.c2 >= 0) store8(dst + m.c2 * 8, z);
+        } else {
+          if (scale) {
+            divide(u, by);
+            if (m.c2 >= 0) divide(z, by);
+          }
+          TC *dst = reinterpret_cast<TC *>((m.is_v ? a.p.values : a.p.keys) + pl.off +
+                                           m.head * a.p.head_stride);
+          store8(dst + m.c * 8, u);
+          if (m.c2 >= 0) store8(dst + m.c2 * 8, z);
+        }
       }
-    }
-    if (is_q) {
-      TI *dst = reinterpret_cast<TI *>(a.q_out + r * a.q_out_stride) + head * a.p.dim;
-      store8(dst + c * 8, x);
-      if (c2 >= 0) store8(dst + c2 * 8, y);
-    } else {
-      const float *scale = is_v ? a.p.value_scale : a.p.key_scale;
-      if (scale) {
-        const float by = __ldg(scale + head);
-        divide(x, by);
-        if (c2 >= 0) divide(y, by);
-      }
-      TC *dst = reinterpret_cast<TC *>((is_v ? a.p.values : a.p.keys) + pl.off +
-                                       head * a.p.head_stride);
-      store8(dst + c * 8, x);
-      if (c2 >= 0) store8(dst + c2 * 8, y);
     }
   }
 }
 
+template <typename TI, typename TC, int ROWS>
+cudaError_t launch_rows(const AppendArgs &a, cudaStream_t st) {
+  const int per_row = items_of_row(a);
+  int groups = 256 / per_row;  // rows side by side, where a row has few items
+  groups = groups < 1 ? 1 : groups * ROWS > kMaxBlock ? kMaxBlock / ROWS : groups;
+  // as many threads a row as even rounds over its items take
+  const int rounds = (per_row + kMaxThreads - 1) / kMaxThreads;
+  const int per_group = (per_row + rounds - 1) / rounds, block = groups * ROWS;
+  int threads = (groups * per_group + 31) / 32 * 32;
+  if (threads < 64) threads = 64;
+  // one wave of CTAs, in whole blocks
+  const int wave = 148 * (1024 / threads < 2 ? 2 : 1024 / threads);
+  int chunk = (a.rows + wave - 1) / wave;
+  chunk = (chunk + block - 1) / block * block;
+  if (chunk > kMaxChunk) chunk = kMaxChunk / block * block;
+  return launch_k(true, k_append<TI, TC, ROWS>, dim3((a.rows + chunk - 1) / chunk), dim3(threads),
+                  0, st, a, chunk, per_row, groups, per_group);
+}
+
+// Several rows a thread keep the memory busy (as many as 32 registers of raw
+// elements hold); with fewer rows than would fill the SMs so, one.
 template <typename TI, typename TC>
 cudaError_t launch(const AppendArgs &a, cudaStream_t st) {
-  const int D8 = a.p.dim / 8, H8 = a.rotary / 16;
-  const int per_row = (a.heads + a.p.kv_heads) * (a.pairs ? D8 : D8 - H8) + a.p.kv_heads * D8;
-  int per_cta = 256 / per_row;
-  per_cta = per_cta < 1 ? 1 : per_cta > kMaxRowsPerCta ? kMaxRowsPerCta : per_cta;
-  // as many threads as even rounds over the items take
-  const int items = per_cta * per_row, rounds = (items + 383) / 384;
-  int threads = ((items + rounds - 1) / rounds + 31) / 32 * 32;
-  if (threads < 64) threads = 64;
-  const int grid = (a.rows + per_cta - 1) / per_cta;
-  return launch_k(true, k_append<TI, TC>, dim3(grid), dim3(threads), 0, st, a, per_cta);
+  constexpr int kRows = sizeof(TI) == 2 ? 4 : 2;
+  return a.rows >= kRows * 296 ? launch_rows<TI, TC, kRows>(a, st) : launch_rows<TI, TC, 1>(a, st);
 }
 
 template <typename TI>
