@@ -17,8 +17,9 @@ namespace fwpkm {
 namespace {
 
 constexpr int kMaxThreads = 512;
-constexpr int kMaxBlock = 8;     // rows of a block
-constexpr int kMaxChunk = 256;   // rows of a CTA
+constexpr int kMaxRows = 8;  // rows of a CTA of k_append_few
+// Items of a head, over all rows, from which k_append_many is the faster one.
+constexpr int kManyThreads = 2048;
 constexpr int kMaxPairs = FWPKM_CACHE_MAX_DIM / 2;
 
 struct Eight {
@@ -124,175 +125,219 @@ __device__ __forceinline__ void divide(Eight &e, float by) {
   for (int i = 0; i < 8; ++i) e.x[i] = __fdiv_rn(e.x[i], by);
 }
 
-// What a thread does of a row: 8 elements of a head or, in a head rotated by
-// halves, two groups of 8 that turn together.
-struct Item {
-  bool is_q, is_v;
-  int head, c, c2;  // c: group of 8; c2: its partner, or -1
-};
-__device__ __forceinline__ Item item_of(const AppendArgs &a, int it) {
-  const int D8 = a.p.dim / 8, H8 = a.rotary / 16;
-  const int turned = a.pairs ? D8 : D8 - H8;  // items of a query or key head
-  const int qk = (a.heads + a.p.kv_heads) * turned;
-  Item m;
-  m.is_v = it >= qk;
-  m.is_q = false;
-  m.c2 = -1;
-  if (m.is_v) {
-    m.head = (it - qk) / D8;
-    m.c = (it - qk) - m.head * D8;
-  } else {
-    m.head = it / turned;
-    m.c = it - m.head * turned;
-    m.is_q = m.head < a.heads;  // queries first
-    if (!m.is_q) m.head -= a.heads;
-    if (!a.pairs) {
-      if (m.c < H8) m.c2 = m.c + H8;
-      else m.c += H8;  // behind the rotated elements
-    }
-  }
-  return m;
+// cos and sin of position p times frequency f, in turns reduced to [-1/2, 1/2]:
+// 1 / (2 pi) in 64 bits.
+__device__ __forceinline__ float2 turn_of(int p, float f) {
+  const double t = (double)p * (double)f * 0.15915494309189533577;
+  float2 w;
+  sincospif(2.f * (float)(t - rint(t)), &w.y, &w.x);
+  return w;
 }
-int items_of_row(const AppendArgs &a) {
-  const int D8 = a.p.dim / 8, H8 = a.rotary / 16;
-  return (a.heads + a.p.kv_heads) * (a.pairs ? D8 : D8 - H8) + a.p.kv_heads * D8;
+__device__ __forceinline__ void rotate(float &u, float &z, const float2 &w) {
+  const float u0 = u;
+  u = fmaf(u0, w.x, -z * w.y);
+  z = fmaf(z, w.x, u0 * w.y);
 }
 
-// A CTA takes `chunk` consecutive rows in blocks of groups x ROWS, a thread the
-// same items of ROWS rows of a block.  Finding where a row goes takes dependent
-// loads: a thread to a row, all of the CTA's rows at once.  In the loop a
-// block's elements are loaded, all rows' at once, before the next block's angles
-// are computed, so the memory is busy meanwhile.
-template <typename TI, typename TC, int ROWS>
-__global__ void __launch_bounds__(kMaxThreads, 2)
-    k_append(const __grid_constant__ AppendArgs a, int chunk, int per_row, int groups,
-             int per_group) {
-  __shared__ Place place[kMaxChunk];
-  __shared__ float2 turn[2][kMaxBlock * kMaxPairs];  // (cos, sin) of a block's angles
+// What a thread does of a row's head: 8 elements or, in a head rotated by
+// halves, two groups of 8 that turn together.  A query or key head has
+// lanes_of() such items, a value head is shared out over the same ones.
+struct Item {
+  int c, c2;  // groups of 8; c2 may be -1
+};
+FWPKM_HD int lanes_of(const AppendArgs &a) {
+  return a.pairs ? a.p.dim / 8 : a.p.dim / 8 - a.rotary / 16;
+}
+__device__ __forceinline__ Item item_of(const AppendArgs &a, int i, bool value) {
+  if (value) {
+    const int c2 = i + lanes_of(a);
+    return {i, c2 < a.p.dim / 8 ? c2 : -1};
+  }
+  if (a.pairs) return {i, -1};
+  const int H8 = a.rotary / 16;
+  return i < H8 ? Item{i, i + H8} : Item{i + H8, -1};  // rotated; behind the rotated elements
+}
+// Heads of a row in the order queries, keys, values.
+template <typename TI>
+__device__ __forceinline__ const TI *head_of(const AppendArgs &a, int64_t row, int h) {
+  const char *base = a.q + row * a.q_stride;
+  if (h >= a.heads) {
+    h -= a.heads;
+    base = a.k + row * a.k_stride;
+    if (h >= a.p.kv_heads) {
+      h -= a.p.kv_heads;
+      base = a.v + row * a.v_stride;
+    }
+  }
+  return reinterpret_cast<const TI *>(base) + h * a.p.dim;
+}
+// Stores a finished item of head h.
+template <typename TI, typename TC>
+__device__ __forceinline__ void put(const AppendArgs &a, int64_t row, const Place &pl, int h,
+                                    const Item &m, Eight &u, Eight &z) {
+  if (h < a.heads) {
+    if (pl.pos < 0) return;
+    TI *dst = reinterpret_cast<TI *>(a.q_out + row * a.q_out_stride) + h * a.p.dim;
+    store8(dst + m.c * 8, u);
+    if (m.c2 >= 0) store8(dst + m.c2 * 8, z);
+    return;
+  }
+  if (pl.off < 0) return;
+  h -= a.heads;
+  const bool value = h >= a.p.kv_heads;
+  if (value) h -= a.p.kv_heads;
+  const float *scale = value ? a.p.value_scale : a.p.key_scale;
+  if (scale) {
+    const float by = __ldg(scale + h);
+    divide(u, by);
+    if (m.c2 >= 0) divide(z, by);
+  }
+  TC *dst = reinterpret_cast<TC *>((value ? a.p.values : a.p.keys) + pl.off + h * a.p.head_stride);
+  store8(dst + m.c * 8, u);
+  if (m.c2 >= 0) store8(dst + m.c2 * 8, z);
+}
+
+// Few rows: a CTA to a row (or several small ones), a thread to an item of a
+// head, the angles shared through shared memory.  What counts is the latency:
+// the elements are loaded before the row's place is looked up.
+template <typename TI, typename TC>
+__global__ void __launch_bounds__(kMaxThreads)
+    k_append_few(const __grid_constant__ AppendArgs a, int per_cta, int per_row) {
+  __shared__ Place place[kMaxRows];
+  __shared__ float2 turn[kMaxRows * kMaxPairs];  // (cos, sin) of each row's angles
   griddep_wait();
   griddep_launch();
-  const int r0 = blockIdx.x * chunk, rows = min(chunk, a.rows - r0);
-  const int block = groups * ROWS, half = a.rotary / 2;
-  const int group = threadIdx.x / per_group, it0 = threadIdx.x - group * per_group;
-  for (int i = threadIdx.x; i < rows; i += blockDim.x) place[i] = find_place(a, r0 + i);
-  __syncthreads();
-  auto angles = [&](int b0) {
-    const int n = min(block, rows - b0) * half;
-    float2 *to = turn[b0 / block & 1];
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const int row = i / half, j = i - row * half;
-      // in turns, reduced to [-1/2, 1/2]: 1 / (2 pi) in 64 bits
-      const double t = (double)max(place[b0 + row].pos, 0) * (double)__ldg(a.freqs + j) *
-                       0.15915494309189533577;
-      float sn, cs;
-      sincospif(2.f * (float)(t - rint(t)), &sn, &cs);
-      to[i] = make_float2(cs, sn);
+  const int r0 = blockIdx.x * per_cta, rows = min(per_cta, a.rows - r0);
+  const int lanes = lanes_of(a), half = a.rotary / 2;
+  const int rotated = a.heads + a.p.kv_heads;
+  bool first = true;
+  for (int n = threadIdx.x;; n += blockDim.x) {
+    const bool live = n < rows * per_row;
+    const int row = n / per_row, it = n - row * per_row, h = it / lanes, i = it - h * lanes;
+    Item m{0, -1};
+    Raw<TI> x, y;
+    if (live) {
+      m = item_of(a, i, h >= rotated);
+      const TI *src = head_of<TI>(a, r0 + row, h);
+      x = load8(src + m.c * 8);
+      if (m.c2 >= 0) y = load8(src + m.c2 * 8);
     }
-  };
-  angles(0);
-  for (int b0 = 0; b0 < rows; b0 += block) {
-    const float2 *at = turn[b0 / block & 1];
-    bool first = true;
-    for (int it = it0;; it += per_group) {
-      const bool live = group < groups && it < per_row;
-      Item m{};
-      Raw<TI> x[ROWS], y[ROWS];
-      if (live) {
-        m = item_of(a, it);
-        const char *base = m.is_v ? a.v : m.is_q ? a.q : a.k;
-        const int64_t stride = m.is_v ? a.v_stride : m.is_q ? a.q_stride : a.k_stride;
+    if (first) {
+      if (threadIdx.x < rows) place[threadIdx.x] = find_place(a, r0 + threadIdx.x);
+      __syncthreads();
+      for (int j = threadIdx.x; j < rows * half; j += blockDim.x)
+        turn[j] = turn_of(max(place[j / half].pos, 0), __ldg(a.freqs + j % half));
+      __syncthreads();
+      first = false;
+    }
+    if (!live) break;
+    Eight u = unpack(x), z;
+    if (m.c2 >= 0) z = unpack(y);
+    if (h < rotated) {
+      if (a.pairs) {
+        if (i < a.rotary / 8)
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) {
-          const int row = b0 + group + j * groups;
-          if (row >= rows) continue;
-          const TI *src =
-              reinterpret_cast<const TI *>(base + (r0 + row) * stride) + m.head * a.p.dim;
-          x[j] = load8(src + m.c * 8);
-          if (m.c2 >= 0) y[j] = load8(src + m.c2 * 8);
-        }
-      }
-      if (first) {
-        __syncthreads();  // this block's angles are there, the last block's are used
-        if (b0 + block < rows) angles(b0 + block);
-        first = false;
-      }
-      if (!live) break;
-      const float *scale = m.is_q ? nullptr : m.is_v ? a.p.value_scale : a.p.key_scale;
-      const float by = scale ? __ldg(scale + m.head) : 1.f;
+          for (int e = 0; e < 4; ++e)
+            rotate(u.x[2 * e], u.x[2 * e + 1], turn[row * half + i * 4 + e]);
+      } else if (m.c2 >= 0) {
 #pragma unroll
-      for (int j = 0; j < ROWS; ++j) {
-        const int row = group + j * groups;
-        if (b0 + row >= rows) continue;
-        const Place pl = place[b0 + row];
-        if (m.is_q ? pl.pos < 0 : pl.off < 0) continue;
-        Eight u = unpack(x[j]), z;
-        if (m.c2 >= 0) {
-          z = unpack(y[j]);
-          const float4 *t = reinterpret_cast<const float4 *>(at + row * half + m.c * 8);
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float4 w = t[e / 2];
-            const float u0 = u.x[e], z0 = z.x[e], u1 = u.x[e + 1], z1 = z.x[e + 1];
-            u.x[e] = u0 * w.x - z0 * w.y;
-            z.x[e] = z0 * w.x + u0 * w.y;
-            u.x[e + 1] = u1 * w.z - z1 * w.w;
-            z.x[e + 1] = z1 * w.z + u1 * w.w;
-          }
-        } else if (!m.is_v && a.pairs && m.c < a.rotary / 8) {
-          const float2 *t = at + row * half + m.c * 4;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 w = t[e];
-            const float u0 = u.x[2 * e], z0 = u.x[2 * e + 1];
-            u.x[2 * e] = u0 * w.x - z0 * w.y;
-            u.x[2 * e + 1] = z0 * w.x + u0 * w.y;
-          }
-        }
-        if (m.is_q) {
-          TI *dst = reinterpret_cast<TI *>(a.q_out + (r0 + b0 + row) * a.q_out_stride) +
-                    m.head * a.p.dim;
-          store8(dst + m.c * 8, u);
-          if (m.c2 >= 0) store8(dst + m.c2 * 8, z);
-        } else {
-          if (scale) {
-            divide(u, by);
-            if (m.c2 >= 0) divide(z, by);
-          }
-          TC *dst = reinterpret_cast<TC *>((m.is_v ? a.p.values : a.p.keys) + pl.off +
-                                           m.head * a.p.head_stride);
-          store8(dst + m.c * 8, u);
-          if (m.c2 >= 0) store8(dst + m.c2 * 8, z);
-        }
+        for (int e = 0; e < 8; ++e) rotate(u.x[e], z.x[e], turn[row * half + i * 8 + e]);
       }
     }
+    put<TI, TC>(a, r0 + row, place[row], h, m, u, z);
   }
 }
 
-template <typename TI, typename TC, int ROWS>
-cudaError_t launch_rows(const AppendArgs &a, cudaStream_t st) {
-  const int per_row = items_of_row(a);
-  int groups = 256 / per_row;  // rows side by side, where a row has few items
-  groups = groups < 1 ? 1 : groups * ROWS > kMaxBlock ? kMaxBlock / ROWS : groups;
-  // as many threads a row as even rounds over its items take
-  const int rounds = (per_row + kMaxThreads - 1) / kMaxThreads;
-  const int per_group = (per_row + rounds - 1) / rounds, block = groups * ROWS;
-  int threads = (groups * per_group + 31) / 32 * 32;
-  if (threads < 64) threads = 64;
-  // one wave of CTAs, in whole blocks
-  const int wave = 148 * (1024 / threads < 2 ? 2 : 1024 / threads);
-  int chunk = (a.rows + wave - 1) / wave;
-  chunk = (chunk + block - 1) / block * block;
-  if (chunk > kMaxChunk) chunk = kMaxChunk / block * block;
-  return launch_k(true, k_append<TI, TC, ROWS>, dim3((a.rows + chunk - 1) / chunk), dim3(threads),
-                  0, st, a, chunk, per_row, groups, per_group);
+// Many rows: a thread to an item of a row, for all of the row's heads or, with
+// several splits, a share of them.  Its angles are the same for all heads: they
+// stay in registers, each computed once, and no thread waits for another.
+// kBatch heads' elements are loaded at once.
+template <typename TI, typename TC, bool PAIRS>
+__global__ void __launch_bounds__(256, 2)
+    k_append_many(const __grid_constant__ AppendArgs a, int splits) {
+  constexpr int kBatch = sizeof(TI) == 2 ? 6 : 3;
+  griddep_wait();
+  griddep_launch();
+  const int lanes = lanes_of(a);
+  const int64_t n = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int row = (int)(n / lanes), i = (int)(n - (int64_t)row * lanes);
+  if (row >= a.rows) return;
+  const int all = a.heads + 2 * a.p.kv_heads, rotated = a.heads + a.p.kv_heads;
+  const Item turned = item_of(a, i, false), copied = item_of(a, i, true);
+  Raw<TI> x[kBatch], y[kBatch];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = h0 + j * splits;
+      if (h >= all) break;
+      const Item m = h < rotated ? turned : copied;
+      const TI *src = head_of<TI>(a, row, h);
+      x[j] = load8(src + m.c * 8);
+      if (m.c2 >= 0) y[j] = load8(src + m.c2 * 8);
+    }
+  };
+  int h0 = blockIdx.y;
+  load(h0);
+  const Place pl = find_place(a, row);
+  constexpr int kTurns = PAIRS ? 4 : 8;
+  const bool turns = PAIRS ? i < a.rotary / 8 : turned.c2 >= 0;
+  float2 w[kTurns];
+  if (turns)
+#pragma unroll
+    for (int e = 0; e < kTurns; ++e) w[e] = turn_of(max(pl.pos, 0), __ldg(a.freqs + i * kTurns + e));
+  while (true) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = h0 + j * splits;
+      if (h >= all) break;
+      const Item m = h < rotated ? turned : copied;
+      Eight u = unpack(x[j]), z;
+      if (m.c2 >= 0) z = unpack(y[j]);
+      if (h < rotated && turns) {
+#pragma unroll
+        for (int e = 0; e < kTurns; ++e) {
+          if (PAIRS) rotate(u.x[2 * (e % 4)], u.x[2 * (e % 4) + 1], w[e]);
+          else rotate(u.x[e], z.x[e], w[e]);
+        }
+      }
+      put<TI, TC>(a, row, pl, h, m, u, z);
+    }
+    h0 += kBatch * splits;
+    if (h0 >= all) break;
+    load(h0);
+  }
 }
 
-// Several rows a thread keep the memory busy (as many as 32 registers of raw
-// elements hold); with fewer rows than would fill the SMs so, one.
 template <typename TI, typename TC>
 cudaError_t launch(const AppendArgs &a, cudaStream_t st) {
-  constexpr int kRows = sizeof(TI) == 2 ? 4 : 2;
-  return a.rows >= kRows * 296 ? launch_rows<TI, TC, kRows>(a, st) : launch_rows<TI, TC, 1>(a, st);
+  const int lanes = lanes_of(a), all = a.heads + 2 * a.p.kv_heads;
+  const int64_t threads = (int64_t)a.rows * lanes;
+  if (threads >= kManyThreads) {
+    // the splits of the heads that take the least time: rounds of two CTAs an
+    // SM, times the heads of a split and what its angles cost beside them
+    const int64_t ctas = (threads + 255) / 256;
+    int splits = 1;
+    int64_t best = INT64_MAX;
+    for (int n = 1; n <= all && n <= 64; ++n) {
+      const int64_t time = (ctas * n + 295) / 296 * ((all + n - 1) / n + 8);
+      if (time < best) {
+        best = time;
+        splits = n;
+      }
+    }
+    const dim3 grid((unsigned)ctas, splits);
+    return a.pairs ? launch_k(true, k_append_many<TI, TC, true>, grid, dim3(256), 0, st, a, splits)
+                   : launch_k(true, k_append_many<TI, TC, false>, grid, dim3(256), 0, st, a, splits);
+  }
+  const int per_row = all * lanes;
+  int per_cta = 256 / per_row;  // rows of a CTA, where a row has few items
+  per_cta = per_cta < 1 ? 1 : per_cta > kMaxRows ? kMaxRows : per_cta;
+  // as many threads as even rounds over the items take
+  const int items = per_cta * per_row, rounds = (items + kMaxThreads - 1) / kMaxThreads;
+  int size = ((items + rounds - 1) / rounds + 31) / 32 * 32;
+  if (size < 64) size = 64;
+  return launch_k(true, k_append_few<TI, TC>, dim3((a.rows + per_cta - 1) / per_cta), dim3(size), 0,
+                  st, a, per_cta, per_row);
 }
 
 template <typename TI>
