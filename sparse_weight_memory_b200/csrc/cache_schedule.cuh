@@ -88,6 +88,11 @@ FWPKM_HD int64_t tile_unit(int j) { return j == 0 ? 0 : (int64_t)j + kSegmentUni
 FWPKM_HD int tile_from(int64_t u) {
   return u == 0 ? 0 : u <= kSegmentUnits ? 1 : (int)(u - kSegmentUnits);
 }
+// Tiles of a segment of `count` that lie before unit u of it.
+FWPKM_HD int tiles_before(int64_t u, int count) {
+  return u <= 0 ? 0 : u <= kSegmentUnits + 1 ? 1 : u - kSegmentUnits < count ? (int)(u - kSegmentUnits)
+                                                                             : count;
+}
 // The line of `total` units cut into `warps` pieces: `more` of q + 1 units,
 // then the others of q.
 struct Line {

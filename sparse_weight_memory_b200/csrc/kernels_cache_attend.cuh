@@ -655,20 +655,23 @@ struct Lengths {
 // A tile's place on the line.
 struct Cursor {
   int b, hr, tile;  // sequence, cached head * blocks + block, tile of the segment
+  int left;         // tiles of the segment in the warp's piece, from this one on
   Span s;
+  int64_t seg;      // first unit of the segment
   __device__ __forceinline__ void enter(const Lengths &len, int tile_tokens) {
     s = cache_span(len(b), len.a.window, tile_tokens);
   }
-  // To the next tile; returns how many units further it is.
-  __device__ __forceinline__ int next(const Lengths &len, int tile_tokens) {
-    if (++tile < s.count) return tile == 1 ? kSegmentUnits + 1 : 1;
-    const int step = s.count == 1 ? kSegmentUnits + 1 : 1;
-    tile = 0;
+  // To the next segment, in a piece that ends before unit `end`.
+  __device__ __forceinline__ void next_segment(const Lengths &len, int tile_tokens, int64_t end) {
+    seg += segment_units(s.count);
+    tile = left = 0;
+    if (seg >= end) return;
     if (++hr == len.a.p.kv_heads * len.a.blocks) {
       hr = 0;
-      if (++b < len.a.s.B) enter(len, tile_tokens);
+      ++b;
+      enter(len, tile_tokens);
     }
-    return step;
+    left = tiles_before(end - seg, s.count);
   }
 };
 
@@ -761,8 +764,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   const long long u0 = busy ? line_cut(line, w) : 0;
   const long long u1 = busy ? line_cut(line, w + 1) : 0;
 
-  Cursor at{};          // the tile that is computed
-  long long unit = u1;  // its unit; from u1 on there is none
+  Cursor at{};  // the tile that is computed; at.left == 0: none is left
   if (busy) {
     // the thread whose sequences u0 falls into: the last one with so many before it
     int i = 0;
@@ -778,24 +780,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
     }
     const long long n = segment_units(at.s.count);
     at.hr = (int)((u0 - p) / n);
-    p += at.hr * n;
-    at.tile = tile_from(u0 - p);
-    unit = p + tile_unit(at.tile);
-    if (at.tile >= at.s.count) {  // behind the segment's last tile: the next segment
-      unit = p + n;
-      at.tile = at.s.count - 1;
-      at.next(lengths, TT);
-    }
+    at.seg = p + at.hr * n;
+    at.tile = tile_from(u0 - at.seg);
+    at.left = tiles_before(u1 - at.seg, at.s.count) - at.tile;
+    if (at.tile >= at.s.count) at.next_segment(lengths, TT, u1);  // behind its last tile
   }
 
   // the segment that the CTA's first warp is in the middle of: k_join's CTAs share it
   if (threadIdx.x == 0) {
     int4 id = make_int4(0, 0, -1, 0);
-    if (unit < u1 && at.tile > 0) {
-      const long long s = unit - tile_unit(at.tile);
-      id = make_int4(at.b, at.hr, line_owner(line, s + tile_unit(at.s.count - 1)),
-                     line_owner(line, s));
-    }
+    if (at.left > 0 && at.tile > 0)
+      id = make_int4(at.b, at.hr, line_owner(line, at.seg + tile_unit(at.s.count - 1)),
+                     line_owner(line, at.seg));
     a.middles[blockIdx.x] = id;
   }
 
@@ -805,8 +801,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   constexpr int kRows = CPR <= 32 ? 32 / CPR : 1;  // rows an instruction copies,
   constexpr int kSteps = CPR <= 32 ? 1 : CPR / 32;  // or instructions that a row takes
   const int cpr = a.p.dim * ESZ / 16;
-  Cursor ld = at;          // the tile that is loaded
-  long long ld_unit = unit;
+  const bool packed = cpr == CPR && a.p.row_stride == TY::DP * ESZ;  // rows without gaps
+  Cursor ld = at;  // the tile that is loaded
   int token = 0, page = -1;  // of this lane's row
   bool seen = false;
   auto look = [&] {
@@ -836,7 +832,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
       even = vis == FULL && first + TT <= a.p.page_size;
       if (even) off = __shfl_sync(FULL, off, 0) + lane_off;
     }
-    if (even) {
+    if (even && packed) {
+      const char *src = pool + off;
+      const uint32_t dst = lane_dst + slot * L::kUnit;
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i)
+        cp_async16(dst + (i / kSteps) * kRows * TY::PITCH + (i % kSteps) * 512, src + i * 512);
+    } else if (even) {
       const char *src = pool + off;
       const int64_t step = kRows * a.p.row_stride;
       const uint32_t dst = lane_dst + slot * L::kUnit;
@@ -858,13 +860,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
       }
     }
   };
-  if (ld_unit < u1) look();
+  if (ld.left > 0) look();
   auto advance = [&](int slot) {
-    if (ld_unit < u1) {
+    if (ld.left > 0) {
       load(slot);
       if (values) {
-        ld_unit += ld.next(lengths, TT);
-        if (ld_unit < u1) look();
+        ++ld.tile;
+        if (--ld.left == 0 && ld.tile == ld.s.count) ld.next_segment(lengths, TT, u1);
+        if (ld.left > 0) look();
       }
       values = !values;
     }
@@ -878,7 +881,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   ty.reset();
   int rows = 0;
   bool fresh = true, whole = at.tile == 0;
-  long long seg = unit - tile_unit(at.tile);
   auto park = [&](int slot) {
     ty.total();
     float4 *dst = reinterpret_cast<float4 *>(a.parts + (int64_t)slot * L::kPart) + lane;
@@ -891,10 +893,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   };
 
   int4 tail = make_int4(0, 0, -1, 0);
-  bool open = false;  // a part is left in the registers
+  bool open = false;  // a part is left in the registers,
+  long long seg = 0;  // of the segment that begins at this unit
   int slot = 0;
   bool second = false;  // the tile's values are next
-  while (unit < u1) {
+  while (at.left > 0) {
     if (fresh) {
       const int h = at.hr / a.blocks, first = (at.hr % a.blocks) * HEADS;
       rows = min(HEADS, a.group - first);
@@ -910,31 +913,33 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
       ty.scores(src, bits[warp][slot]);
     } else {
       ty.outputs(src);
-      const bool end = at.tile + 1 == at.s.count;
-      const int b = at.b, hr = at.hr;
-      const int count = at.s.count;
-      unit += at.next(lengths, TT);
       open = true;
-      if (end) {
-        if (whole) {
-          const int64_t r = first_row(b, hr);
-          ty.finish(reinterpret_cast<Out *>(a.out) + r * a.p.dim, a.lse ? a.lse + r : nullptr,
-                    rows, a.p.dim, a.p.value_scale ? __ldg(a.p.value_scale + hr / a.blocks) : 1.f);
-          open = false;
-        } else if (unit < u1) {
-          park(2 * w);
-          open = false;
+      ++at.tile;
+      if (--at.left == 0) {  // the segment or the piece ends
+        const int b = at.b, hr = at.hr, count = at.s.count;
+        const bool end = at.tile == count;
+        seg = at.seg;
+        if (end) {
+          at.next_segment(lengths, TT, u1);
+          if (whole) {
+            const int64_t r = first_row(b, hr);
+            ty.finish(reinterpret_cast<Out *>(a.out) + r * a.p.dim, a.lse ? a.lse + r : nullptr,
+                      rows, a.p.dim, a.p.value_scale ? __ldg(a.p.value_scale + hr / a.blocks) : 1.f);
+            open = false;
+          } else if (at.left > 0) {
+            park(2 * w);
+            open = false;
+          }
+          if (at.left > 0) {
+            ty.reset();
+            fresh = whole = true;
+          }
         }
-        if (unit < u1) {
-          ty.reset();
-          fresh = whole = true;
-          seg = unit;
+        if (at.left == 0 && open) {  // what is left is joined with the CTA's other warps'
+          const int last = line_owner(line, seg + tile_unit(count - 1));
+          if (lane == 0) last_at[warp] = make_int4(b, hr, last, whole);
+          if (whole && !end) tail = make_int4(b, hr, last, 0);
         }
-      }
-      if (unit >= u1 && open) {  // what is left is joined with the CTA's other warps'
-        const int last = line_owner(line, seg + tile_unit(count - 1));
-        if (lane == 0) last_at[warp] = make_int4(b, hr, last, whole);
-        if (whole && !end) tail = make_int4(b, hr, last, 0);
       }
     }
     second = !second;

@@ -35,6 +35,7 @@ int per_cta(int64_t total, int most, int ctas) { return line_per_cta(cache_line(
 int64_t units(int tiles) { return segment_units(tiles); }
 int64_t unit_of(int j) { return tile_unit(j); }
 int from(int64_t u) { return tile_from(u); }
+int tiles(int64_t u, int count) { return tiles_before(u, count); }
 int page(int d, int t) { return page_of(page_div(d), t); }
 int length(int len, int width, int page, int *bad) {
   bool b; int r = cache_length(len, width, page, b); *bad = b; return r;
@@ -58,7 +59,7 @@ def sched(tmp_path_factory):
     L.warps.argtypes, L.cut.argtypes = [i64, i32], [i64, i32, i32]
     L.per_cta.argtypes = [i64, i32, i32]
     L.owner.argtypes, L.from_ = [i64, i32, i64], getattr(L, "from")
-    L.from_.argtypes = [i64]
+    L.from_.argtypes, L.tiles.argtypes = [i64], [i64, i32]
     L.cut.restype = L.units.restype = L.unit_of.restype = i64
     return L
 
@@ -113,6 +114,8 @@ def test_pieces_share_the_line_out(sched):
             for w in range(owner[0], owner[-1] + 1):  # where the warp enters the segment
                 j = sched.from_(max(0, cuts[w] - int(first)))
                 assert j == int(np.searchsorted(owner, w))
+                end = sched.tiles(cuts[w + 1] - int(first), c)
+                assert end == int(np.searchsorted(owner, w, side="right"))
 
 
 def test_largest_line_stays_within_64_bits(sched):
