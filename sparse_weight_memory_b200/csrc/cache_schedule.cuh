@@ -5,18 +5,19 @@
 //
 // A tile is TT consecutive tokens of one sequence (aligned to TT), a segment
 // all visible tiles of one sequence for one cached head and one block of the
-// query heads that share it.  A segment costs its tiles and kSegmentUnits
-// tiles' worth beside them (its queries, its result): so many units.  Segments
-// are laid end to end in the order (sequence, cached head, block), and the line
-// of all units is cut into `warps` pieces whose sizes differ by at most one
-// unit.  A warp takes the tiles whose first unit lies in its piece: tile 0 of a
-// segment is at the segment's first unit, tile j at unit kSegmentUnits + j.
+// query heads that share it.  A segment costs its tiles and `extra` tiles' worth
+// beside them (its queries, its result): so many units.  Segments are laid end
+// to end in the order (sequence, cached head, block), and the line of all units
+// is cut into `warps` pieces whose sizes differ by at most one unit.  A warp
+// takes the tiles whose first unit lies in its piece: tile 0 of a segment is at
+// the segment's first unit, tile j at unit extra + j.  Where there are no more
+// tiles than warps, each is a piece of its own (extra = 0): the shortest time.
 // A segment that a cut falls into is summed in parts:
 //   - the part that begins with the segment lies in the tail slot 2w+1 of its
 //     warp w,
 //   - the part of each later warp w' lies in that warp's head slot 2w'.
 // So a segment's parts are slots 2w+1, 2(w+1), ..., 2*last (no warp between
-// them is without a tile, since pieces have more than kSegmentUnits units).
+// them is without a tile, since pieces have more than `extra` units).
 #pragma once
 #include <stdint.h>
 
@@ -78,32 +79,28 @@ FWPKM_HD Span cache_span(int len, int window, int tile) {
   return s;
 }
 
-constexpr int kSegmentUnits = 2;
-constexpr int kLeastUnits = kSegmentUnits + 2;  // smaller pieces are not worth a warp
-
-FWPKM_HD int64_t segment_units(int tiles) { return (int64_t)tiles + kSegmentUnits; }
 // Unit of tile j, and the first tile at or after unit u of the segment (which
 // may be its number of tiles: none).
-FWPKM_HD int64_t tile_unit(int j) { return j == 0 ? 0 : (int64_t)j + kSegmentUnits; }
-FWPKM_HD int tile_from(int64_t u) {
-  return u == 0 ? 0 : u <= kSegmentUnits ? 1 : (int)(u - kSegmentUnits);
+FWPKM_HD int64_t tile_unit(int j, int extra) { return j == 0 ? 0 : (int64_t)j + extra; }
+FWPKM_HD int tile_from(int64_t u, int extra) {
+  return u == 0 ? 0 : u <= extra ? 1 : (int)(u - extra);
 }
 // Tiles of a segment of `count` that lie before unit u of it.
-FWPKM_HD int tiles_before(int64_t u, int count) {
-  return u <= 0 ? 0 : u <= kSegmentUnits + 1 ? 1 : u - kSegmentUnits < count ? (int)(u - kSegmentUnits)
-                                                                             : count;
+FWPKM_HD int tiles_before(int64_t u, int count, int extra) {
+  return u <= 0 ? 0 : u <= extra + 1 ? 1 : u - extra < count ? (int)(u - extra) : count;
 }
-// The line of `total` units cut into `warps` pieces: `more` of q + 1 units,
-// then the others of q.
+// The line of the units of all tiles and segments, cut into `warps` pieces:
+// `more` of q + 1 units, then the others of q.
 struct Line {
-  int64_t total, q;
-  int warps, more;
+  int64_t q;
+  int warps, more, extra;
 };
-FWPKM_HD Line cache_line(int64_t total, int most) {
-  const int64_t w = total / kLeastUnits;
+FWPKM_HD Line cache_line(int64_t tiles, int64_t segments, int most) {
   Line l;
-  l.total = total;
-  l.warps = w < 1 ? 1 : w < most ? (int)w : most;
+  l.extra = tiles <= most ? 0 : 2;
+  const int64_t total = tiles + l.extra * segments;
+  const int64_t w = total / (l.extra ? l.extra + 2 : 1);  // smaller pieces are not worth a warp
+  l.warps = w < most ? (int)w : most;
   l.q = total / l.warps;
   l.more = (int)(total - l.q * l.warps);
   return l;
@@ -116,10 +113,10 @@ FWPKM_HD int line_owner(const Line &l, int64_t unit) {
   return unit < big ? (int)(unit / (l.q + 1)) : l.more + (int)((unit - big) / l.q);
 }
 // Warps of a CTA that take pieces: few pieces are spread over the CTAs, but not
-// thinner than four to a CTA, whose sums join in shared memory.
-FWPKM_HD int line_per_cta(const Line &l, int ctas) {
+// thinner than `least` to a CTA, whose sums join in shared memory.
+FWPKM_HD int line_per_cta(const Line &l, int ctas, int least) {
   const int n = (l.warps + ctas - 1) / ctas;
-  return n < 4 ? 4 : n;
+  return n < least ? least : n;
 }
 
 }  // namespace fwpkm

@@ -190,7 +190,7 @@ namespace {
 
 // The workspace: parts, their (m, l), the tails and middles.
 struct Workspace {
-  int64_t ml, tails, middles, per, bytes;
+  int64_t ml, tails, middles, bytes;
 };
 Workspace layout(int cache_dtype, int dim, int group) {
   const AttendShape s = attend_shape(cache_dtype, dim, group);
@@ -199,8 +199,7 @@ Workspace layout(int cache_dtype, int dim, int group) {
   w.ml = 2 * warps * s.part * (int64_t)sizeof(float);
   w.tails = w.ml + 2 * warps * s.heads * (int64_t)sizeof(float2);
   w.middles = w.tails + warps * (int64_t)sizeof(int4);
-  w.per = w.middles + kAttendCtas * (int64_t)sizeof(int4);
-  w.bytes = w.per + kAttendCtas * (int64_t)sizeof(int);
+  w.bytes = w.middles + kAttendCtas * (int64_t)sizeof(int4);
   return w;
 }
 
@@ -259,7 +258,6 @@ extern "C" fwpkm_status fwpkm_cache_attend(const fwpkm_cache *cache,
   a.ml = reinterpret_cast<float2 *>(ws + w.ml);
   a.tails = reinterpret_cast<int4 *>(ws + w.tails);
   a.middles = reinterpret_cast<int4 *>(ws + w.middles);
-  a.per = reinterpret_cast<int *>(ws + w.per);
   a.errors = device_errors;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.heads = heads;

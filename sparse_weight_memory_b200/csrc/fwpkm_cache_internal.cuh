@@ -60,10 +60,9 @@ struct AttendArgs {
   float *lse;
   float *parts;  // [2 * warps][part] sums o of the segments' parts
   float2 *ml;    // [2 * warps][heads] their (m, l)
-  int4 *tails;   // [warps] (sequence, head * blocks + block, last warp) of the segment whose
-                 // first part is the warp's tail slot; last warp -1: none
+  int4 *tails;   // [CTAs][warps] (sequence, head * blocks + block, last warp, pieces of a CTA) of
+                 // the segment whose first part is the warp's tail slot; last warp -1: none
   int4 *middles; // [CTAs] (.., last warp, first warp) of the one its first warp is inside of
-  int *per;      // [CTAs] pieces of a CTA, the same for all
   unsigned *errors;
   float scale_log2;  // scale * log2(e)
   int heads, group, blocks;  // group: query heads of a cached head, in `blocks` segments

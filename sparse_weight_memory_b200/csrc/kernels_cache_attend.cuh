@@ -35,6 +35,8 @@ namespace attend {
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLeastFactor = 1.18e-38f;  // a factor that no score feels, but not 0
+// Warps of a CTA that take pieces, at the least (where it has so many).
+constexpr int kLeastPerCta = 8;
 // A score may exceed the reference by this (base 2) before the sums are scaled
 // to a new one: weights stay under 2^(kShift + kSlack).
 constexpr float kSlack = 6.f;
@@ -471,167 +473,174 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
 
 // f32: the products run as plain 32-bit multiply-adds, which hold the full
 // accuracy; RR heads take RR of them an element, 8 flops a byte at 8 heads, a
-// third of what the SMs can do in the time of the bytes.  A lane has V = DP/32
-// elements of every head's query and output.  The tile's 8 x RR products of a
-// token and a head, each spread over the lanes, are summed by halving: 31
-// exchanges for 32 sums, after which lane i has sum i.
+// third of what the SMs can do in the time of the bytes.  A group of LG lanes
+// has two of the heads, a lane of it DP/LG elements of their queries and outputs
+// (in pieces of 4, the group's side by side).  A lane's sums of its elements, 8
+// tokens x 2 heads, are summed over the group by halving: each step exchanges
+// half of what a lane has left.
 template <int DP_, int RR_>
 struct F32 {
   using Out = float;
   static constexpr int DP = DP_, TT = 8, HEADS = RR_, RR = RR_, ESZ = 4, PITCH = DP * 4;
   static constexpr int kDtype = FWPKM_F32;
-  static constexpr int V = DP / 32, NS = 8 * RR / 32;  // NS scores a lane
-  static constexpr int VP = V < 4 ? V : 4;             // elements of one shared load
-  static constexpr int kParts = RR * V / 4 > 0 ? (RR * V + 3) / 4 : 1;
-  static_assert(RR == 4 || RR == 8, "8 tokens x RR heads are whole warps of scores");
-  float q[RR][V], o[RR][V];
-  float c, m, l;  // of head lane % RR (each lane of a head: its own tokens' sum)
+  static constexpr int LG = 64 / RR, V4 = DP / LG / 4;  // lanes of a group, pieces of a lane
+  static constexpr int NS = 16 / LG;                    // scores of a lane: tokens of one head
+  static constexpr int kParts = 2 * V4;
+  static_assert(RR == 4 || RR == 8, "groups of 16 or 8 lanes");
+  float q[2][V4][4], o[2][V4][4];
+  float c, m, l;  // of head head(); l: of the lane's own tokens
   float p[NS];
+  int dim;
 
-  // Elements of this lane: VP consecutive ones, then the same 128 further on.
-  __device__ __forceinline__ static int elem(int lane, int v) {
-    return (v / VP) * 32 * VP + lane * VP + v % VP;
+  __device__ __forceinline__ static int lane() { return threadIdx.x & 31; }
+  // After the halving lane j of a group has sums j*NS .. of its 16, in the order
+  // head (2), token (8).
+  __device__ __forceinline__ static int head() {
+    return lane() / LG * 2 + (lane() % LG) * NS / 8;
   }
+  __device__ __forceinline__ static int token() { return (lane() % LG) * NS % 8; }
   __device__ __forceinline__ void reset() {
     m = kNegInf;
     l = 0.f;
 #pragma unroll
-    for (int h = 0; h < RR; ++h)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int v = 0; v < V; ++v) o[h][v] = 0.f;
+      for (int i = 0; i < V4; ++i) o[h][i][0] = o[h][i][1] = o[h][i][2] = o[h][i][3] = 0.f;
   }
-  __device__ __forceinline__ void load_q(const char *qp, int rows, int dim, float f) {
-    const int lane = threadIdx.x & 31;
+  __device__ __forceinline__ void load_q(const char *qp, int rows, int dim_, float f) {
+    dim = dim_;
 #pragma unroll
-    for (int h = 0; h < RR; ++h)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = elem(lane, v);
-        const float x =
-            h < rows && e < dim ? __ldg(reinterpret_cast<const float *>(qp) + h * dim + e) : 0.f;
-        q[h][v] = f < 0.f ? -x : x;
+      for (int i = 0; i < V4; ++i) {
+        const int row = lane() / LG * 2 + h, e = (i * LG + lane() % LG) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < rows && e < dim)
+          v = __ldg(reinterpret_cast<const float4 *>(qp + (row * dim + e) * 4));
+        const float sign = f < 0.f ? -1.f : 1.f;
+        q[h][i][0] = v.x * sign;
+        q[h][i][1] = v.y * sign;
+        q[h][i][2] = v.z * sign;
+        q[h][i][3] = v.w * sign;
       }
     c = fmaxf(fabsf(f), kLeastFactor);
   }
-  __device__ __forceinline__ static void row(float (&x)[V], uint32_t a) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < V / VP; ++i) {
-      const uint32_t at = a + (i * 32 + lane) * VP * 4;
-      if constexpr (VP == 4)
-        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(x[i * 4]), "=f"(x[i * 4 + 1]), "=f"(x[i * 4 + 2]), "=f"(x[i * 4 + 3])
-                     : "r"(at)
-                     : "memory");
-      else
-        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
-                     : "=f"(x[i * 2]), "=f"(x[i * 2 + 1])
-                     : "r"(at)
-                     : "memory");
-    }
+  __device__ __forceinline__ static void lds4(float (&x)[4], uint32_t a) {
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                 : "r"(a)
+                 : "memory");
   }
   __device__ __forceinline__ void scores(uint32_t ks, unsigned vis) {
-    const int lane = threadIdx.x & 31;
-    constexpr int TS = 32 / RR;  // tokens whose products make 32 sums
-    float s[NS];
+    const uint32_t a0 = ks + lane() % LG * 16;
+    float x[16] = {};
+#pragma unroll
+    for (int i = 0; i < V4; ++i) {
+      if (i * LG * 4 >= dim) break;  // (only zeros from here on)
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        float k[4];
+        lds4(k, a0 + t * PITCH + i * LG * 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[h * 8 + t] = fmaf(q[h][i][e], k[e], x[h * 8 + t]);
+      }
+    }
+#pragma unroll
+    for (int w = LG / 2, n = 8; w > 0; w >>= 1, n >>= 1) {
+      const bool up = lane() & w;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float keep = up ? x[i + n] : x[i], give = up ? x[i] : x[i + n];
+        x[i] = keep + __shfl_xor_sync(FULL, give, w);
+      }
+    }
+    float top = kNegInf;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-      float x[32];
-#pragma unroll
-      for (int t = 0; t < TS; ++t) {
-        float k[V];
-        row(k, ks + (j * TS + t) * PITCH);
-#pragma unroll
-        for (int h = 0; h < RR; ++h) {
-          float a = q[h][0] * k[0];
-#pragma unroll
-          for (int v = 1; v < V; ++v) a = fmaf(q[h][v], k[v], a);
-          x[t * RR + h] = a;
-        }
-      }
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) {
-        const bool up = lane & w;
-#pragma unroll
-        for (int i = 0; i < w; ++i) {
-          const float keep = up ? x[i + w] : x[i], give = up ? x[i] : x[i + w];
-          x[i] = keep + __shfl_xor_sync(FULL, give, w);
-        }
-      }
-      s[j] = (vis >> (j * TS + lane / RR)) & 1u ? x[0] : kNegInf;
+      if (!((vis >> (token() + j)) & 1u)) x[j] = kNegInf;
+      top = fmaxf(top, x[j]);
     }
-    float top = s[0];
-#pragma unroll
-    for (int j = 1; j < NS; ++j) top = fmaxf(top, s[j]);
     if (__any_sync(FULL, fmaf(top, c, -m) > kSlack)) {
 #pragma unroll
-      for (int w = RR; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, w));
+      for (int w = 4 / NS; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, w));
       top = fmaxf(m, top * c);
       const float f = ex2(m - (top == kNegInf ? 0.f : top));
       m = top;
       l *= f;
 #pragma unroll
-      for (int h = 0; h < RR; ++h) {
-        const float fh = __shfl_sync(FULL, f, h);
+      for (int h = 0; h < 2; ++h) {
+        const float fh = __shfl_sync(FULL, f, h * (LG / 2), LG);
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[h][v] *= fh;
+        for (int i = 0; i < V4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][i][e] *= fh;
       }
     }
     const float u = m == kNegInf ? 0.f : m;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-      p[j] = ex2(fmaf(s[j], c, -u));
+      p[j] = ex2(fmaf(x[j], c, -u));
       l += p[j];
     }
   }
   __device__ __forceinline__ void outputs(uint32_t vs) {
-    constexpr int TS = 32 / RR;
+    const uint32_t a0 = vs + lane() % LG * 16;
+    float w[2][8];
 #pragma unroll
-    for (int j = 0; j < NS; ++j)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int t = 0; t < TS; ++t) {
-        float x[V];
-        row(x, vs + (j * TS + t) * PITCH);
+      for (int t = 0; t < 8; ++t) w[h][t] = __shfl_sync(FULL, p[t % NS], (h * 8 + t) / NS, LG);
 #pragma unroll
-        for (int h = 0; h < RR; ++h) {
-          const float w = __shfl_sync(FULL, p[j], t * RR + h);
+    for (int i = 0; i < V4; ++i) {
+      if (i * LG * 4 >= dim) break;
 #pragma unroll
-          for (int v = 0; v < V; ++v) o[h][v] = fmaf(w, x[v], o[h][v]);
-        }
+      for (int t = 0; t < 8; ++t) {
+        float v[4];
+        lds4(v, a0 + t * PITCH + i * LG * 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][i][e] = fmaf(w[h][t], v[e], o[h][i][e]);
       }
+    }
   }
   __device__ __forceinline__ void total() {
 #pragma unroll
-    for (int w = RR; w < 32; w <<= 1) l += __shfl_xor_sync(FULL, l, w);
+    for (int w = 4 / NS; w > 0; w >>= 1) l += __shfl_xor_sync(FULL, l, w);
   }
   __device__ __forceinline__ float4 part(int i) const {
-    float x[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = o[(i * 4 + e) / V][(i * 4 + e) % V];
+    const float(&x)[4] = o[i / V4][i % V4];
     return make_float4(x[0], x[1], x[2], x[3]);
   }
   template <typename F>
   __device__ __forceinline__ void stats(F &&f) const {
-    if ((threadIdx.x & 31) < RR) f(threadIdx.x & 31, m, l);
+    if (token() == 0) f(head(), m, l);
   }
-  __device__ __forceinline__ static int head_of(int i, int, int e) { return (i * 4 + e) / V; }
-  __device__ __forceinline__ static int col_of(int i, int lane, int e) {
-    return elem(lane, (i * 4 + e) % V);
+  __device__ __forceinline__ static int head_of(int i, int ln, int) { return ln / LG * 2 + i / V4; }
+  __device__ __forceinline__ static int col_of(int i, int ln, int e) {
+    return (i % V4 * LG + ln % LG) * 4 + e;
   }
-  __device__ __forceinline__ void finish(float *out, float *lse, int rows, int dim, float vs) {
+  __device__ __forceinline__ void finish(float *out, float *lse, int rows, int, float vs) {
     total();
-    const int lane = threadIdx.x & 31;
     const float inv = l == 0.f ? 0.f : vs / l;
 #pragma unroll
-    for (int h = 0; h < RR; ++h) {
-      const float f = __shfl_sync(FULL, inv, h);
+    for (int h = 0; h < 2; ++h) {
+      const float f = __shfl_sync(FULL, inv, h * (LG / 2), LG);
+      const int row = lane() / LG * 2 + h;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = elem(lane, v);
-        if (h < rows && e < dim) out[h * dim + e] = o[h][v] * f;
+      for (int i = 0; i < V4; ++i) {
+        const int e = (i * LG + lane() % LG) * 4;
+        if (row < rows && e < dim)
+          *reinterpret_cast<float4 *>(out + row * dim + e) =
+              make_float4(o[h][i][0] * f, o[h][i][1] * f, o[h][i][2] * f, o[h][i][3] * f);
       }
     }
-    if (lse && lane < rows) lse[lane] = log_sum(m, l);
+    if (lse)
+      stats([&](int h, float mh, float lh) {
+        if (h < rows) lse[h] = log_sum(mh, lh);
+      });
   }
 };
 
@@ -662,8 +671,9 @@ struct Cursor {
     s = cache_span(len(b), len.a.window, tile_tokens);
   }
   // To the next segment, in a piece that ends before unit `end`.
-  __device__ __forceinline__ void next_segment(const Lengths &len, int tile_tokens, int64_t end) {
-    seg += segment_units(s.count);
+  __device__ __forceinline__ void next_segment(const Lengths &len, int tile_tokens, int64_t end,
+                                               int extra) {
+    seg += (int64_t)s.count + extra;
     tile = left = 0;
     if (seg >= end) return;
     if (++hr == len.a.p.kv_heads * len.a.blocks) {
@@ -671,7 +681,7 @@ struct Cursor {
       ++b;
       enter(len, tile_tokens);
     }
-    left = tiles_before(end - seg, s.count);
+    left = tiles_before(end - seg, s.count, extra);
   }
 };
 
@@ -688,10 +698,22 @@ template <typename TY, int WARPS, int UNITS>
 struct Layout {
   static constexpr int kUnit = TY::TT * TY::PITCH;  // a tile's keys, or its values
   static constexpr int kRing = UNITS * kUnit;
-  static constexpr int kSmem = WARPS * kRing;
   static constexpr int kPart = TY::kParts * 128;  // floats of a part
+  struct Side {
+    long long before[WARPS * 32 + 1];  // tiles before each thread's sequences
+    long long wsum[WARPS];
+    long long last_seg[WARPS];  // first unit of the segment a warp ended in, or -1
+    int4 last_at[WARPS];        // (sequence, head and block, the segment's last warp, begins)
+    float2 last_ml[WARPS][TY::HEADS];  // of a warp; then, at a run's first warp, of the run
+    float weight[WARPS][TY::HEADS];
+    float end_weight[WARPS][TY::HEADS];
+    int run_at[WARPS];
+    int kept[WARPS * 32];         // lengths of the first sequences
+    unsigned bits[WARPS][UNITS];  // visible tokens of the tile whose keys are there
+  };
+  static constexpr int kSmem = WARPS * kRing + (int)sizeof(Side);
   static_assert(kRing >= kPart * 4, "a warp's sums fit its ring");
-  static_assert(kSmem <= 222 * 1024, "shared memory of an SM, less the static part");
+  static_assert(kRing % 16 == 0 && kSmem <= 232448, "the shared memory that a CTA may have");
 };
 
 template <typename TY, int WARPS, int UNITS>
@@ -700,17 +722,16 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   using Out = typename TY::Out;
   constexpr int TT = TY::TT, ESZ = TY::ESZ, HEADS = TY::HEADS;
   extern __shared__ __align__(128) char smem[];
-  __shared__ long long before[WARPS * 32 + 1];  // units before each thread's sequences
-  __shared__ long long wsum[WARPS];
-  __shared__ int kept[WARPS * 32];  // lengths of the first sequences
-  __shared__ unsigned bits[WARPS][UNITS];  // visible tokens of the tile whose keys are there
-  __shared__ long long last_seg[WARPS];    // first unit of the segment a warp ended in, or -1
-  __shared__ int4 last_at[WARPS];  // (sequence, head and block, the segment's last warp, begins)
-  __shared__ float2 last_ml[WARPS][HEADS];
-  __shared__ float weight[WARPS][HEADS];
-  __shared__ float2 run_ml[WARPS][HEADS];
-  __shared__ float end_weight[WARPS][HEADS];
-  __shared__ int run_at[WARPS];
+  typename L::Side &side = *reinterpret_cast<typename L::Side *>(smem + WARPS * L::kRing);
+  auto &before = side.before;
+  auto &kept = side.kept;
+  auto &bits = side.bits;
+  auto &last_seg = side.last_seg;
+  auto &last_at = side.last_at;
+  auto &last_ml = side.last_ml;
+  auto &weight = side.weight;
+  auto &end_weight = side.end_weight;
+  auto &run_at = side.run_at;
 
   static_assert(WARPS <= 16, "a half warp sums over the warps");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -737,7 +758,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
       const int len = Lengths::get(a, b, bad);
       if (bad && blockIdx.x == 0 && a.errors) atomicOr(a.errors, (unsigned)FWPKM_CACHE_BAD_LENGTH);
       if (b < WARPS * 32) kept[b] = len;
-      mine += segment_units(cache_span(len, a.window, TT).count);
+      mine += cache_span(len, a.window, TT).count;
     }
     mine *= hrs;
     long long sum = mine;
@@ -746,9 +767,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
       const long long up = __shfl_up_sync(FULL, sum, o);
       if (lane >= o) sum += up;
     }
-    if (lane == 31) wsum[warp] = sum;
+    if (lane == 31) side.wsum[warp] = sum;
     __syncthreads();
-    long long base = lane < warp ? wsum[lane] : 0;
+    long long base = lane < warp ? side.wsum[lane] : 0;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) base += __shfl_xor_sync(FULL, base, o);
     base = __shfl_sync(FULL, base, 0);
@@ -757,8 +778,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
     __syncthreads();
   }
   const Lengths lengths{a, kept, WARPS * 32};
-  const Line line = cache_line(before[WARPS * 32], gridDim.x * WARPS);
-  const int per = line_per_cta(line, gridDim.x);  // pieces of a CTA
+  const Line line = cache_line(before[WARPS * 32], (long long)a.s.B * hrs, gridDim.x * WARPS);
+  const int per = line_per_cta(line, gridDim.x, kLeastPerCta);  // pieces of a CTA
+  static_assert(kLeastPerCta <= WARPS, "no more than it has");
+  const long long seq_extra = (long long)line.extra * hrs;  // of a sequence's segments
   const int w0 = blockIdx.x * per, w = w0 + warp;
   const bool busy = warp < per && w < line.warps;
   const long long u0 = busy ? line_cut(line, w) : 0;
@@ -767,30 +790,31 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   Cursor at{};  // the tile that is computed; at.left == 0: none is left
   if (busy) {
     // the thread whose sequences u0 falls into: the last one with so many before it
+    auto units = [&](int i) { return before[i] + seq_extra * min(i * chunk, a.s.B); };
     int i = 0;
-    if (WARPS > 1) i = __popc(__ballot_sync(FULL, lane < WARPS && before[lane * 32] <= u0)) - 1;
-    i = i * 32 + __popc(__ballot_sync(FULL, before[i * 32 + lane] <= u0)) - 1;
-    long long p = before[i];
+    if (WARPS > 1) i = __popc(__ballot_sync(FULL, lane < WARPS && units(lane * 32) <= u0)) - 1;
+    i = i * 32 + __popc(__ballot_sync(FULL, units(i * 32 + lane) <= u0)) - 1;
+    long long p = units(i);
     at.b = i * chunk;
     at.enter(lengths, TT);
-    while (p + segment_units(at.s.count) * hrs <= u0) {
-      p += segment_units(at.s.count) * hrs;
+    while (p + (long long)at.s.count * hrs + seq_extra <= u0) {
+      p += (long long)at.s.count * hrs + seq_extra;
       ++at.b;
       at.enter(lengths, TT);
     }
-    const long long n = segment_units(at.s.count);
+    const long long n = at.s.count + line.extra;
     at.hr = (int)((u0 - p) / n);
     at.seg = p + at.hr * n;
-    at.tile = tile_from(u0 - at.seg);
-    at.left = tiles_before(u1 - at.seg, at.s.count) - at.tile;
-    if (at.tile >= at.s.count) at.next_segment(lengths, TT, u1);  // behind its last tile
+    at.tile = tile_from(u0 - at.seg, line.extra);
+    at.left = tiles_before(u1 - at.seg, at.s.count, line.extra) - at.tile;
+    if (at.tile >= at.s.count) at.next_segment(lengths, TT, u1, line.extra);  // behind its last
   }
 
   // the segment that the CTA's first warp is in the middle of: k_join's CTAs share it
   if (threadIdx.x == 0) {
     int4 id = make_int4(0, 0, -1, 0);
     if (at.left > 0 && at.tile > 0)
-      id = make_int4(at.b, at.hr, line_owner(line, at.seg + tile_unit(at.s.count - 1)),
+      id = make_int4(at.b, at.hr, line_owner(line, at.seg + tile_unit(at.s.count - 1, line.extra)),
                      line_owner(line, at.seg));
     a.middles[blockIdx.x] = id;
   }
@@ -866,7 +890,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
       load(slot);
       if (values) {
         ++ld.tile;
-        if (--ld.left == 0 && ld.tile == ld.s.count) ld.next_segment(lengths, TT, u1);
+        if (--ld.left == 0 && ld.tile == ld.s.count) ld.next_segment(lengths, TT, u1, line.extra);
         if (ld.left > 0) look();
       }
       values = !values;
@@ -920,7 +944,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
         const bool end = at.tile == count;
         seg = at.seg;
         if (end) {
-          at.next_segment(lengths, TT, u1);
+          at.next_segment(lengths, TT, u1, line.extra);
           if (whole) {
             const int64_t r = first_row(b, hr);
             ty.finish(reinterpret_cast<Out *>(a.out) + r * a.p.dim, a.lse ? a.lse + r : nullptr,
@@ -936,7 +960,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
           }
         }
         if (at.left == 0 && open) {  // what is left is joined with the CTA's other warps'
-          const int last = line_owner(line, seg + tile_unit(count - 1));
+          const int last = line_owner(line, seg + tile_unit(count - 1, line.extra));
           if (lane == 0) last_at[warp] = make_int4(b, hr, last, whole);
           if (whole && !end) tail = make_int4(b, hr, last, 0);
         }
@@ -955,8 +979,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
     for (int i = 0; i < TY::kParts; ++i) mine[i * 32] = ty.part(i);
     ty.stats([&](int h, float m, float l) { last_ml[warp][h] = make_float2(m, l); });
   }
-  if (lane == 0 && warp < per) a.tails[w] = tail;
-  if (threadIdx.x == 0) a.per[blockIdx.x] = per;
+  tail.w = per;
+  if (lane == 0) a.tails[blockIdx.x * WARPS + warp] = tail;
   if (!__syncthreads_or(open)) return;
   // A run is the neighbouring warps whose last parts are of one segment; its
   // first warp's slot takes its sum.  Bit k of `heads`: warp k begins a run.
@@ -990,7 +1014,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
     }
     const float f = ex2(end.x - u);
     l = fmaf(end.y, f, l);
-    run_ml[k0][h] = make_float2(top, l);
+    last_ml[k0][h] = make_float2(top, l);
     end_weight[k0][h] = more ? f : 0.f;
   }
   __syncthreads();
@@ -1031,18 +1055,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int c = TY::col_of(i, ln, e);
-        const float2 ml = run_ml[k0][h[e]];
+        const float2 ml = last_ml[k0][h[e]];
         if (h[e] < n && c < a.p.dim)
           reinterpret_cast<Out *>(a.out)[(r + h[e]) * a.p.dim + c] =
               to_out<Out>(ml.y == 0.f ? 0.f : x[e] * (vs / ml.y));
         if (a.lse && h[e] < n && c == 0) a.lse[r + h[e]] = log_sum(ml.x, ml.y);
       }
-      if (q == 0) a.tails[w0 + k0].z = -1;
+      if (q == 0) a.tails[blockIdx.x * WARPS + k0].z = -1;
     } else {
       reinterpret_cast<float4 *>(a.parts + (int64_t)to * L::kPart)[q] =
           make_float4(x[0], x[1], x[2], x[3]);
       if (q < HEADS) {
-        a.ml[to * HEADS + q] = run_ml[k0][q];
+        a.ml[to * HEADS + q] = last_ml[k0][q];
         // the slot that k_join may look for at the run's last warp holds nothing
         if (k1 - k0 > 1) a.ml[2 * (w0 + k1 - 1) * HEADS + q] = make_float2(kNegInf, 0.f);
       }
@@ -1054,7 +1078,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
 // warps have a part share a segment's groups of 32 x 4 floats out; a group with
 // few parts is one warp's, one with many is summed by all warps of the CTA.
 constexpr int kJoinWarps = 16, kJoinFew = 6;
-template <typename TY>
+template <typename TY, int WARPS>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const __grid_constant__ AttendArgs a) {
   using Out = typename TY::Out;
   constexpr int HEADS = TY::HEADS, kPart = TY::kParts * 128;
@@ -1062,15 +1086,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const __grid_constant_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
   griddep_launch();
-  const int cta = blockIdx.x, per = a.per[cta], w0 = cta * per;
   // lane i: the segment that begins in warp i; lane 31: the one that goes on here
+  const int cta = blockIdx.x;
   int4 mine = make_int4(0, 0, -1, 0);
-  if (lane < per) {
-    mine = a.tails[w0 + lane];
-    mine.w = w0 + lane;
-  } else if (lane == 31) {
-    mine = a.middles[cta];
-  }
+  if (lane < WARPS) mine = a.tails[cta * WARPS + lane];
+  else if (lane == 31) mine = a.middles[cta];
+  const int per = __shfl_sync(FULL, mine.w, 0);
+  if (lane < WARPS) mine.w = cta * per + lane;
   unsigned left = __ballot_sync(FULL, mine.z >= 0);
   int turn = 0;  // single-warp groups dealt out so far
   for (; left; left &= left - 1) {
@@ -1192,7 +1214,7 @@ cudaError_t prepare() {
                              cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_join<TY>, cudaFuncAttributePreferredSharedMemoryCarveout,
+    e = cudaFuncSetAttribute(k_join<TY, WARPS>, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
@@ -1209,7 +1231,7 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
   e = launch_k(true, k_attend<TY, WARPS, UNITS>, dim3(kAttendCtas), dim3(WARPS * 32),
                Layout<TY, WARPS, UNITS>::kSmem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_k(true, k_join<TY>, dim3(kAttendCtas), dim3(kJoinWarps * 32), 0,
+  return launch_k(true, k_join<TY, WARPS>, dim3(kAttendCtas), dim3(kJoinWarps * 32), 0,
                   st, a);
 }
 

@@ -28,14 +28,19 @@ void span(int len, int window, int tile, int *o) {
   Span s = cache_span(len, window, tile);
   o[0] = s.lo; o[1] = s.len; o[2] = s.first; o[3] = s.count;
 }
-int warps(int64_t total, int most) { return cache_line(total, most).warps; }
-int64_t cut(int64_t total, int most, int w) { return line_cut(cache_line(total, most), w); }
-int owner(int64_t total, int most, int64_t unit) { return line_owner(cache_line(total, most), unit); }
-int per_cta(int64_t total, int most, int ctas) { return line_per_cta(cache_line(total, most), ctas); }
-int64_t units(int tiles) { return segment_units(tiles); }
-int64_t unit_of(int j) { return tile_unit(j); }
-int from(int64_t u) { return tile_from(u); }
-int tiles(int64_t u, int count) { return tiles_before(u, count); }
+void line(int64_t tiles, int64_t segments, int most, int ctas, int least, int64_t *o) {
+  Line l = cache_line(tiles, segments, most);
+  o[0] = l.warps; o[1] = l.extra; o[2] = line_per_cta(l, ctas, least);
+}
+int64_t cut(int64_t tiles, int64_t segments, int most, int w) {
+  return line_cut(cache_line(tiles, segments, most), w);
+}
+int owner(int64_t tiles, int64_t segments, int most, int64_t unit) {
+  return line_owner(cache_line(tiles, segments, most), unit);
+}
+int64_t unit_of(int j, int extra) { return tile_unit(j, extra); }
+int from(int64_t u, int extra) { return tile_from(u, extra); }
+int tiles(int64_t u, int count, int extra) { return tiles_before(u, count, extra); }
 int page(int d, int t) { return page_of(page_div(d), t); }
 int length(int len, int width, int page, int *bad) {
   bool b; int r = cache_length(len, width, page, b); *bad = b; return r;
@@ -56,11 +61,11 @@ def sched(tmp_path_factory):
                     "-static-libubsan", "-shared", "-fPIC", "-I", fwbuild.CSRC,
                     str(d / "shim.cpp"), "-o", so], check=True)
     L = ctypes.CDLL(so)
-    L.warps.argtypes, L.cut.argtypes = [i64, i32], [i64, i32, i32]
-    L.per_cta.argtypes = [i64, i32, i32]
-    L.owner.argtypes, L.from_ = [i64, i32, i64], getattr(L, "from")
-    L.from_.argtypes, L.tiles.argtypes = [i64], [i64, i32]
-    L.cut.restype = L.units.restype = L.unit_of.restype = i64
+    L.line.argtypes = [i64, i64, i32, i32, i32, ctypes.POINTER(i64)]
+    L.cut.argtypes, L.owner.argtypes = [i64, i64, i32, i32], [i64, i64, i32, i64]
+    L.unit_of.argtypes, L.from_ = [i32, i32], getattr(L, "from")
+    L.from_.argtypes, L.tiles.argtypes = [i64, i32], [i64, i32, i32]
+    L.cut.restype = L.unit_of.restype = i64
     return L
 
 
@@ -90,39 +95,45 @@ def test_pieces_share_the_line_out(sched):
     most; and a segment's parts are those of its first warp to its last, none
     of them without a tile."""
     rng = np.random.default_rng(0)
-    for round_ in range(150):
+    o = (i64 * 3)()
+    seen = set()
+    for _ in range(200):
         most = int(rng.choice([1, 5, 592, 1184, 2368]))
         big = int(np.exp(rng.uniform(0, np.log(3000))))
         counts = [int(c) for c in rng.integers(1, big + 1, int(rng.integers(1, 60)))]
-        at = np.cumsum([0] + [sched.units(c) for c in counts])
-        total = int(at[-1])
-        n = sched.warps(total, most)
-        cuts = [sched.cut(total, most, w) for w in range(n + 1)]
-        sizes = np.diff(cuts)
-        assert 1 <= n <= most and cuts[0] == 0 and cuts[-1] == total
-        assert sizes.max() - sizes.min() <= 1 and (n == 1 or sizes.min() >= 4)
+        line = (sum(counts), len(counts), most)
         ctas = -(-most // 16)
-        per = sched.per_cta(total, most, ctas)
-        assert per * ctas >= n and per <= max(4, -(-most // ctas))
+        sched.line(*line, ctas, 8, o)
+        n, extra, per = list(o)
+        seen.add(extra)
+        assert extra == (0 if line[0] <= most else 2)
+        assert per * ctas >= n and per <= max(8, -(-most // ctas))
+        at = np.cumsum([0] + [c + extra for c in counts])
+        cuts = [sched.cut(*line, w) for w in range(n + 1)]
+        sizes = np.diff(cuts)
+        assert 1 <= n <= most and cuts[0] == 0 and cuts[-1] == at[-1]
+        assert sizes.max() - sizes.min() <= 1 and (n == 1 or sizes.min() > extra)
         for c, first in zip(counts, at[:-1]):
-            unit = [int(first) + sched.unit_of(j) for j in range(c)]
-            assert unit[-1] < first + sched.units(c)
+            unit = [int(first) + sched.unit_of(j, extra) for j in range(c)]
+            assert unit[-1] < first + c + extra
             owner = np.searchsorted(cuts, unit, side="right") - 1
             for j in {0, c - 1, c // 2}:
-                assert sched.owner(total, most, unit[j]) == owner[j]
+                assert sched.owner(*line, unit[j]) == owner[j]
             assert set(owner) == set(range(owner[0], owner[-1] + 1))
             for w in range(owner[0], owner[-1] + 1):  # where the warp enters the segment
-                j = sched.from_(max(0, cuts[w] - int(first)))
+                j = sched.from_(max(0, cuts[w] - int(first)), extra)
                 assert j == int(np.searchsorted(owner, w))
-                end = sched.tiles(cuts[w + 1] - int(first), c)
+                end = sched.tiles(cuts[w + 1] - int(first), c, extra)
                 assert end == int(np.searchsorted(owner, w, side="right"))
+    assert seen == {0, 2}
 
 
 def test_largest_line_stays_within_64_bits(sched):
-    total = (1 << 22) * ((1 << 28) + 2)  # B * heads times the units of 2^31 tokens
-    assert sched.cut(total, 2368, 2368) == total
-    assert sched.owner(total, 2368, total - 1) == 2367
-    assert sched.owner(total, 2368, 0) == 0
+    line = ((1 << 22) * (1 << 28), 1 << 22, 2368)  # B * heads segments of 2^31 tokens
+    total = line[0] + 2 * line[1]
+    assert sched.cut(*line, 2368) == total
+    assert sched.owner(*line, total - 1) == 2367
+    assert sched.owner(*line, 0) == 0
 
 
 def test_page_of_a_token_is_the_quotient(sched):

@@ -163,6 +163,21 @@ def test_attend(dtype, heads, kv, dim, page):
 
 
 @pytest.mark.parametrize("dtype", [BF, E4, F32])
+@pytest.mark.parametrize("dim", [32, 64, 128, 256])
+@pytest.mark.parametrize("group", [1, 4, 5, 8, 9, 16, 33])
+def test_attend_every_variant(dtype, dim, group):
+    """Each width the kernels are built for, with few and many heads to a cached
+    one, divided one tile to a warp and many."""
+    g = gen(dim + group)
+    for lengths in ([5, 0, 200, 31], [3000, 2900, 1, 700] * 4):
+        table, pages = make_table(g, lengths, 16)
+        cache = make_pool(g, pages, 2, 16, dim, dtype)
+        q = torch.randn((len(lengths), 2 * group, dim), generator=g, device="cuda").to(
+            F32 if dtype == F32 else BF)
+        check(cache, q, table, lengths)
+
+
+@pytest.mark.parametrize("dtype", [BF, E4, F32])
 @pytest.mark.parametrize("window", [1, 7, 16, 100, 999, 1000, 5000])
 def test_attend_window(dtype, window):
     """Pages wholly before the window are gone (-1) and not looked at."""
