@@ -179,10 +179,10 @@ fwpkm::AttendShape fwpkm::attend_shape(int cache_dtype, int dim, int group) {
     const int heads = group <= 4 ? 4 : 8;
     return {dp == 64 ? 16 : dp == 128 ? 12 : 8, heads, heads * dp};
   }
-  const int heads = group <= 8 || dp == 256 ? 8 : 16;
+  const int heads = group <= 8 ? 8 : group <= 16 || dp == 256 ? 16 : 32;
   int warps = 16;
-  if (dp == 128 && heads == 16) warps = 12;
-  if (dp == 256) warps = cache_dtype == FWPKM_BF16 ? 8 : 12;
+  if (dp * heads >= 128 * 16 || (dp == 128 && cache_dtype == FWPKM_E4M3)) warps = 8;
+  else if (dp == 128 || heads > 8) warps = 12;
   return {warps, heads, heads * dp};
 }
 

@@ -126,11 +126,16 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 // What the two tensor-core types share.  Thread (g = lane/4, t = lane%4).  s
 // and p: tokens 16n + g (+ 8), heads 8h + 2t (+ 1), the accumulator layout of
 // mma.m16n8.  o: head elements as rows, heads as columns.
+// QS: the queries lie in shared memory, in the order in which the products take
+// them, where the outputs need the registers.
 template <typename Self, int DP_, int TT_, int NT_>
 struct Mma {
   static constexpr int DP = DP_, TT = TT_, NT = NT_, HEADS = 8 * NT_;
+  static constexpr bool QS = DP * NT > 256;
+  static constexpr int kQuery = QS ? DP / 16 * NT * 256 : 0;  // bytes of a warp's queries
   static constexpr int kParts = DP / 16 * NT;
-  unsigned q[DP / 16][NT][2];
+  unsigned q[QS ? 1 : DP / 16][QS ? 1 : NT][2];
+  char *qs;  // shared memory of this warp's queries
   float c[NT][2], m[NT][2], l[NT][2];
   float o[DP / 16][NT][4];
   unsigned hi[TT / 16][NT][2];
@@ -143,6 +148,20 @@ struct Mma {
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) o[n][h][0] = o[n][h][1] = o[n][h][2] = o[n][h][3] = 0.f;
     }
+  }
+  __device__ __forceinline__ void set_q(int k, int h, unsigned x, unsigned y) {
+    if constexpr (QS) {
+      reinterpret_cast<uint2 *>(qs)[(k * NT + h) * 32 + (threadIdx.x & 31)] = make_uint2(x, y);
+    } else {
+      q[k][h][0] = x;
+      q[k][h][1] = y;
+    }
+  }
+  __device__ __forceinline__ uint2 get_q(int k, int h) const {
+    if constexpr (QS)
+      return reinterpret_cast<const uint2 *>(qs)[(k * NT + h) * 32 + (threadIdx.x & 31)];
+    else
+      return make_uint2(q[k][h][0], q[k][h][1]);
   }
   // s: products; on return weights, in the same places.  kShift: the largest
   // weight is 2^kShift when the reference is new.
@@ -270,21 +289,23 @@ struct Bf16 : Mma<Bf16<DP_, TT_, NT_>, DP_, TT_, NT_> {
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
-      for (int h = 0; h < NT; ++h)
+      for (int h = 0; h < NT; ++h) {
+        unsigned x[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int row = 8 * h + g, c = k * 16 + t * 2 + i * 8;
-          this->q[k][h][i] =
-              row < rows && c < dim
-                  ? flip ^ __ldg(reinterpret_cast<const unsigned *>(qp + (row * dim + c) * 2))
-                  : 0u;
+          x[i] = row < rows && c < dim
+                     ? flip ^ __ldg(reinterpret_cast<const unsigned *>(qp + (row * dim + c) * 2))
+                     : 0u;
         }
+        this->set_q(k, h, x[0], x[1]);
+      }
 #pragma unroll
     for (int h = 0; h < NT; ++h) this->c[h][0] = this->c[h][1] = fmaxf(fabsf(f), kLeastFactor);
   }
-  __device__ __forceinline__ void scores(uint32_t ks, unsigned vis) {
+  __device__ __forceinline__ void scores(const char *ks, unsigned vis) {
     const int lane = threadIdx.x & 31;
-    const uint32_t a0 = ks + ((lane & 7) + ((lane >> 3) & 1) * 8) * PITCH + (lane >> 4) * 16;
+    const uint32_t a0 = smem_u32(ks) + ((lane & 7) + ((lane >> 3) & 1) * 8) * PITCH + (lane >> 4) * 16;
     float s[TT / 16][NT][4] = {};
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k)
@@ -293,7 +314,10 @@ struct Bf16 : Mma<Bf16<DP_, TT_, NT_>, DP_, TT_, NT_> {
         unsigned a[4];
         ldsm4(a, a0 + n * 16 * PITCH + k * 32);
 #pragma unroll
-        for (int h = 0; h < NT; ++h) mma_bf16(s[n][h], a, this->q[k][h][0], this->q[k][h][1]);
+        for (int h = 0; h < NT; ++h) {
+          const uint2 q = this->get_q(k, h);
+          mma_bf16(s[n][h], a, q.x, q.y);
+        }
       }
     this->weigh(s, vis, 0.f);
 #pragma unroll
@@ -309,9 +333,9 @@ struct Bf16 : Mma<Bf16<DP_, TT_, NT_>, DP_, TT_, NT_> {
               pack_bf16(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u)));
         }
   }
-  __device__ __forceinline__ void outputs(uint32_t vs) {
+  __device__ __forceinline__ void outputs(const char *vs) {
     const int lane = threadIdx.x & 31;
-    const uint32_t a0 = vs + ((lane & 7) + (lane >> 4) * 8) * PITCH + ((lane >> 3) & 1) * 16;
+    const uint32_t a0 = smem_u32(vs) + ((lane & 7) + (lane >> 4) * 8) * PITCH + ((lane >> 3) & 1) * 16;
 #pragma unroll
     for (int k = 0; k < TT / 16; ++k)
 #pragma unroll
@@ -367,6 +391,7 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
 #pragma unroll
     for (int h = 0; h < NT; ++h) {
       float top = 0.f;
+      unsigned x[DP / 16][2];
       const int row = 8 * h + g;
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k) {
@@ -374,8 +399,8 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
         uint2 v = make_uint2(0u, 0u);
         if (row < rows && c < dim)
           v = __ldg(reinterpret_cast<const uint2 *>(qp + (row * dim + c) * 2));
-        this->q[k][h][0] = v.x;
-        this->q[k][h][1] = v.y;
+        x[k][0] = v.x;
+        x[k][1] = v.y;
         const float m0 = fmaxf(fabsf(__uint_as_float(v.x << 16)),
                                fabsf(__uint_as_float(v.x & 0xffff0000u)));
         const float m1 = fmaxf(fabsf(__uint_as_float(v.y << 16)),
@@ -392,20 +417,22 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
           __uint_as_float(((unsigned)(254 - e) << 23) | (f < 0.f ? 0x80000000u : 0u));
       const float up = __uint_as_float((unsigned)e << 23);
 #pragma unroll
-      for (int k = 0; k < DP / 16; ++k)
+      for (int k = 0; k < DP / 16; ++k) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          this->q[k][h][i] = pack_f16(__uint_as_float(this->q[k][h][i] << 16) * down,
-                                      __uint_as_float(this->q[k][h][i] & 0xffff0000u) * down);
+          x[k][i] = pack_f16(__uint_as_float(x[k][i] << 16) * down,
+                             __uint_as_float(x[k][i] & 0xffff0000u) * down);
+        this->set_q(k, h, x[k][0], x[k][1]);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i)  // the factors of this thread's columns
         this->c[h][i] =
             fmaxf(fabsf(f) * __shfl_sync(FULL, up, (2 * t + i) * 4), kLeastFactor);
     }
   }
-  __device__ __forceinline__ void scores(uint32_t ks, unsigned vis) {
+  __device__ __forceinline__ void scores(const char *ks, unsigned vis) {
     const int lane = threadIdx.x & 31;
-    const uint32_t a0 = ks + ((lane & 7) + ((lane >> 3) & 1) * 8) * PITCH + (lane >> 4) * 16;
+    const uint32_t a0 = smem_u32(ks) + ((lane & 7) + ((lane >> 3) & 1) * 8) * PITCH + (lane >> 4) * 16;
     float s[TT / 16][NT][4] = {};
 #pragma unroll
     for (int k = 0; k < DP / 32; ++k)
@@ -418,8 +445,10 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
           const unsigned a[4] = {e4m3_f16(b[2 * j]), e4m3_f16(b[2 * j + 1]),
                                  e4m3_f16(b[2 * j] >> 16), e4m3_f16(b[2 * j + 1] >> 16)};
 #pragma unroll
-          for (int h = 0; h < NT; ++h)
-            mma_f16(s[n][h], a, this->q[2 * k + j][h][0], this->q[2 * k + j][h][1]);
+          for (int h = 0; h < NT; ++h) {
+            const uint2 q = this->get_q(2 * k + j, h);
+            mma_f16(s[n][h], a, q.x, q.y);
+          }
         }
       }
     this->weigh(s, vis, kShift);
@@ -431,9 +460,9 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
         for (int i = 0; i < 2; ++i)
           this->hi[n][h][i] = transpose8(pack_f16(s[n][h][2 * i], s[n][h][2 * i + 1]));
   }
-  __device__ __forceinline__ void outputs(uint32_t vs) {
+  __device__ __forceinline__ void outputs(const char *vs) {
     const int lane = threadIdx.x & 31;
-    const uint32_t a0 = vs + (lane & 15) * PITCH + (lane >> 4) * 16;
+    const uint32_t a0 = smem_u32(vs) + (lane & 15) * PITCH + (lane >> 4) * 16;
 #pragma unroll
     for (int k = 0; k < TT / 16; ++k)
 #pragma unroll
@@ -485,12 +514,13 @@ struct F32 {
   static constexpr int kDtype = FWPKM_F32;
   static constexpr int LG = 64 / RR, V4 = DP / LG / 4;  // lanes of a group, pieces of a lane
   static constexpr int NS = 16 / LG;                    // scores of a lane: tokens of one head
-  static constexpr int kParts = 2 * V4;
+  static constexpr int kParts = 2 * V4, kQuery = 0;
   static_assert(RR == 4 || RR == 8, "groups of 16 or 8 lanes");
   float q[2][V4][4], o[2][V4][4];
   float c, m, l;  // of head head(); l: of the lane's own tokens
   float p[NS];
   int dim;
+  char *qs;  // (the queries fit the registers)
 
   __device__ __forceinline__ static int lane() { return threadIdx.x & 31; }
   // After the halving lane j of a group has sums j*NS .. of its 16, in the order
@@ -525,14 +555,15 @@ struct F32 {
       }
     c = fmaxf(fabsf(f), kLeastFactor);
   }
-  __device__ __forceinline__ static void lds4(float (&x)[4], uint32_t a) {
-    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
-                 : "r"(a)
-                 : "memory");
+  __device__ __forceinline__ static void lds4(float (&x)[4], const char *a) {
+    const float4 v = *reinterpret_cast<const float4 *>(a);
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
   }
-  __device__ __forceinline__ void scores(uint32_t ks, unsigned vis) {
-    const uint32_t a0 = ks + lane() % LG * 16;
+  __device__ __forceinline__ void scores(const char *ks, unsigned vis) {
+    const char *a0 = ks + lane() % LG * 16;
     float x[16] = {};
 #pragma unroll
     for (int i = 0; i < V4; ++i) {
@@ -585,8 +616,8 @@ struct F32 {
       l += p[j];
     }
   }
-  __device__ __forceinline__ void outputs(uint32_t vs) {
-    const uint32_t a0 = vs + lane() % LG * 16;
+  __device__ __forceinline__ void outputs(const char *vs) {
+    const char *a0 = vs + lane() % LG * 16;
     float w[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -697,7 +728,7 @@ __device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float x) {
 template <typename TY, int WARPS, int UNITS>
 struct Layout {
   static constexpr int kUnit = TY::TT * TY::PITCH;  // a tile's keys, or its values
-  static constexpr int kRing = UNITS * kUnit;
+  static constexpr int kRing = UNITS * kUnit, kWarp = kRing + TY::kQuery;
   static constexpr int kPart = TY::kParts * 128;  // floats of a part
   struct Side {
     long long before[WARPS * 32 + 1];  // tiles before each thread's sequences
@@ -711,9 +742,9 @@ struct Layout {
     int kept[WARPS * 32];         // lengths of the first sequences
     unsigned bits[WARPS][UNITS];  // visible tokens of the tile whose keys are there
   };
-  static constexpr int kSmem = WARPS * kRing + (int)sizeof(Side);
+  static constexpr int kSmem = WARPS * kWarp + (int)sizeof(Side);
   static_assert(kRing >= kPart * 4, "a warp's sums fit its ring");
-  static_assert(kRing % 16 == 0 && kSmem <= 232448, "the shared memory that a CTA may have");
+  static_assert(kWarp % 16 == 0 && kSmem <= 232448, "the shared memory that a CTA may have");
 };
 
 template <typename TY, int WARPS, int UNITS>
@@ -722,7 +753,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   using Out = typename TY::Out;
   constexpr int TT = TY::TT, ESZ = TY::ESZ, HEADS = TY::HEADS;
   extern __shared__ __align__(128) char smem[];
-  typename L::Side &side = *reinterpret_cast<typename L::Side *>(smem + WARPS * L::kRing);
+  typename L::Side &side = *reinterpret_cast<typename L::Side *>(smem + WARPS * L::kWarp);
   auto &before = side.before;
   auto &kept = side.kept;
   auto &bits = side.bits;
@@ -735,7 +766,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
 
   static_assert(WARPS <= 16, "a half warp sums over the warps");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  char *ring = smem + warp * L::kRing;
+  char *ring = smem + warp * L::kWarp;
   const uint32_t ring_u = smem_u32(ring);
 
   if (a.p.dim < TY::DP) {  // elements behind the head's own: zeros, which no copy touches
@@ -826,7 +857,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   constexpr int kSteps = CPR <= 32 ? 1 : CPR / 32;  // or instructions that a row takes
   const int cpr = a.p.dim * ESZ / 16;
   const bool packed = cpr == CPR && a.p.row_stride == TY::DP * ESZ;  // rows without gaps
-  Cursor ld = at;  // the tile that is loaded
+  Cursor ld = at;  // the tile whose keys are loaded next
   int token = 0, page = -1;  // of this lane's row
   bool seen = false;
   auto look = [&] {
@@ -855,6 +886,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
                : 0;
       even = vis == FULL && first + TT <= a.p.page_size;
       if (even) off = __shfl_sync(FULL, off, 0) + lane_off;
+      // the next tile's pages are looked up while this one's values are loaded
+      ++ld.tile;
+      if (--ld.left == 0 && ld.tile == ld.s.count)
+        ld.next_segment(lengths, TT, u1, line.extra);
+      if (ld.left > 0) look();
     }
     if (even && packed) {
       const char *src = pool + off;
@@ -886,13 +922,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   };
   if (ld.left > 0) look();
   auto advance = [&](int slot) {
-    if (ld.left > 0) {
+    if (ld.left > 0 || values) {
       load(slot);
-      if (values) {
-        ++ld.tile;
-        if (--ld.left == 0 && ld.tile == ld.s.count) ld.next_segment(lengths, TT, u1, line.extra);
-        if (ld.left > 0) look();
-      }
       values = !values;
     }
     cp_commit();
@@ -902,6 +933,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
 
   // ---- the pass --------------------------------------------------------------
   TY ty;
+  ty.qs = ring + L::kRing;
   ty.reset();
   int rows = 0;
   bool fresh = true, whole = at.tile == 0;
@@ -932,7 +964,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
     cp_wait<UNITS - 2>();
     __syncwarp();  // the unit has landed, and the one before it is free
     advance(slot == 0 ? UNITS - 1 : slot - 1);
-    const uint32_t src = ring_u + slot * L::kUnit;
+    const char *src = ring + slot * L::kUnit;
     if (!second) {
       ty.scores(src, bits[warp][slot]);
     } else {
@@ -1037,7 +1069,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
     if (more) end = reinterpret_cast<const float4 *>(a.parts + (int64_t)(2 * id.z) * L::kPart)[q];
 #pragma unroll 4
     for (int k = k0; k < k1; ++k) {
-      const float4 v = reinterpret_cast<const float4 *>(smem + k * L::kRing)[q];
+      const float4 v = reinterpret_cast<const float4 *>(smem + k * L::kWarp)[q];
       x[0] = fmaf(v.x, weight[k][h[0]], x[0]);
       x[1] = fmaf(v.y, weight[k][h[1]], x[1]);
       x[2] = fmaf(v.z, weight[k][h[2]], x[2]);
