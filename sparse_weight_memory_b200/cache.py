@@ -24,6 +24,7 @@ _vp = ctypes.c_void_p
 # the current stream's handle without a Stream object around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class _Cache(ctypes.Structure):  # fwpkm_cache
@@ -109,6 +110,8 @@ class KVCache:
         self._keys, self._values = keys, values
         self._scales = (key_scale, value_scale)
         self.device, self.dtype = keys.device, keys.dtype
+        self._index = keys.get_device()  # -1: not on a CUDA device
+        self._bytes_of = torch.empty(0, dtype=torch.uint8, device=self.device)
         self.pages, self.kv_heads, self.page_size, self.dim = keys.shape
         if values.device != self.device:
             raise FwpkmError(FWPKM_EINVAL, "keys and values must be on one device")
@@ -138,16 +141,19 @@ class KVCache:
     # Each call checks every tensor it hands on; the common case is kept short,
     # since a small call takes less time on the GPU than in here.
     def _on_device(self, t, dtype, name, contiguous=True):
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise FwpkmError(FWPKM_EINVAL, f"{name} is on {t.device}, the cache on {self.device}")
         if contiguous and not t.is_contiguous():
             raise FwpkmError(FWPKM_ESHAPE, f"{name} must be contiguous")
 
     def _batch(self, table, lengths):
-        self._on_device(table, torch.int32, "table", contiguous=False)
-        self._on_device(lengths, torch.int32, "lengths")
+        if table.dtype is not torch.int32 or table.get_device() != self._index:
+            self._on_device(table, torch.int32, "table", contiguous=False)
+        if lengths.dtype is not torch.int32 or lengths.get_device() != self._index or \
+                not lengths.is_contiguous():
+            self._on_device(lengths, torch.int32, "lengths")
         shape = table.shape
         if len(shape) != 2 or lengths.shape != shape[:1] or 0 in shape:
             raise FwpkmError(FWPKM_ESHAPE, "table must be [B][width] and lengths [B], B and width "
@@ -160,16 +166,17 @@ class KVCache:
 
     def _rows(self, t, name, dtype, rows, heads=None):
         """The element stride between the rows of t [rows][heads][dim], each contiguous."""
-        self._on_device(t, dtype, name, contiguous=False)
-        shape = t.shape
-        if len(shape) != 3 or shape[0] != rows or shape[2] != self.dim or \
+        if t.dtype is not dtype or t.get_device() != self._index:
+            self._on_device(t, dtype, name, contiguous=False)
+        shape, dim = t.shape, self.dim
+        if len(shape) != 3 or shape[0] != rows or shape[2] != dim or \
                 (heads is not None and shape[1] != heads):
             raise FwpkmError(FWPKM_ESHAPE, f"{name} must be [{rows}]"
-                             f"[{'heads' if heads is None else heads}][{self.dim}]")
+                             f"[{'heads' if heads is None else heads}][{dim}]")
         step, head, one = t.stride()
-        if one != 1 or (head != self.dim and shape[1] > 1):
+        if one != 1 or (head != dim and shape[1] > 1):
             raise FwpkmError(FWPKM_ESHAPE, f"the rows of {name} must be contiguous")
-        return step if rows > 1 else shape[1] * self.dim
+        return step if rows > 1 else shape[1] * dim
 
     def _errors(self, errors):
         self._on_device(errors, torch.int32, "errors")
@@ -177,12 +184,12 @@ class KVCache:
         return errors.data_ptr()
 
     def _elsewhere(self):
-        return self.device.type == "cuda" and torch.cuda.current_device() != self.device.index
+        return self._index >= 0 and _current_device() != self._index
 
     def _current_stream(self):
-        if self.device.type != "cuda":
+        if self._index < 0:
             raise FwpkmError(FWPKM_EINVAL, f"the cache is on {self.device}, not on a CUDA device")
-        return _raw_stream(self.device.index)
+        return _raw_stream(self._index)
 
     @contextlib.contextmanager
     def _other(self, stream):
@@ -228,7 +235,7 @@ class KVCache:
             q_stride = self._rows(q, "q", dtype, rows)
             heads = q.shape[1]
             if q_out is None:
-                q_out = torch.empty((rows, heads, self.dim), dtype=dtype, device=self.device)
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
                 out_stride = heads * self.dim
             else:
                 out_stride = self._rows(q_out, "q_out", dtype, rows, heads)
@@ -275,7 +282,7 @@ class KVCache:
         heads = q.shape[1]
         need = self.attend_workspace(B, heads)
         if out is None:
-            out = torch.empty((B, heads, self.dim), dtype=dtype, device=self.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
             self._on_device(out, dtype, "out")
             _shape(out.shape == q.shape, "out must be [B][heads][dim]")
@@ -285,7 +292,7 @@ class KVCache:
             _shape(lse.shape == (B, heads), "lse must be [B][heads]")
             lse_at = lse.data_ptr()
         if workspace is None:
-            workspace, size = torch.empty(need, dtype=torch.uint8, device=self.device), need
+            workspace, size = self._bytes_of.new_empty(need), need
         else:
             self._on_device(workspace, torch.uint8, "workspace")
             size = workspace.numel()
