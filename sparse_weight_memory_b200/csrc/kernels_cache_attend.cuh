@@ -96,13 +96,12 @@ __device__ __forceinline__ unsigned pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const unsigned *>(&h);
 }
-// Two 8-bit floats (the low 16 bits of v) as two 16-bit ones, exactly.
-__device__ __forceinline__ unsigned e4m3_f16(unsigned v) {
-  unsigned d;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
-      : "=r"(d)
+// Four 8-bit floats as 16-bit ones, exactly: the low two and the high two.
+__device__ __forceinline__ void e4m3_f16(unsigned v, unsigned &lo, unsigned &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(v));
-  return d;
 }
 __device__ __forceinline__ unsigned transpose8(unsigned a) {  // of an 8 x 8 matrix of 16 bits
   unsigned d;
@@ -442,8 +441,9 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
         ldsm4(b, a0 + n * 16 * PITCH + k * 32);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const unsigned a[4] = {e4m3_f16(b[2 * j]), e4m3_f16(b[2 * j + 1]),
-                                 e4m3_f16(b[2 * j] >> 16), e4m3_f16(b[2 * j + 1] >> 16)};
+          unsigned a[4];
+          e4m3_f16(b[2 * j], a[0], a[2]);
+          e4m3_f16(b[2 * j + 1], a[1], a[3]);
 #pragma unroll
           for (int h = 0; h < NT; ++h) {
             const uint2 q = this->get_q(2 * k + j, h);
@@ -472,9 +472,9 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           // bytes (t, 2g) (t, 2g+1) (t+1, 2g) (t+1, 2g+1): sort by element
-          const unsigned x = __byte_perm(b[2 * j], 0, 0x3120);
-          const unsigned y = __byte_perm(b[2 * j + 1], 0, 0x3120);
-          const unsigned a[4] = {e4m3_f16(x), e4m3_f16(x >> 16), e4m3_f16(y), e4m3_f16(y >> 16)};
+          unsigned a[4];
+          e4m3_f16(__byte_perm(b[2 * j], 0, 0x3120), a[0], a[1]);
+          e4m3_f16(__byte_perm(b[2 * j + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
           for (int h = 0; h < NT; ++h)
             mma_f16(this->o[2 * n + j][h], a, this->hi[k][h][0], this->hi[k][h][1]);
