@@ -18,6 +18,9 @@
 //   - the part of each later warp w' lies in that warp's head slot 2w'.
 // So a segment's parts are slots 2w+1, 2(w+1), ..., 2*last (no warp between
 // them is without a tile, since pieces have more than `extra` units).
+// Where every segment is short, the line is first cut into a piece for each CTA,
+// each cut moved to the next segment's start, and then those pieces for the
+// CTA's warps: no segment lies in two CTAs, and no second kernel is needed.
 #pragma once
 #include <stdint.h>
 
@@ -89,34 +92,32 @@ FWPKM_HD int tile_from(int64_t u, int extra) {
 FWPKM_HD int tiles_before(int64_t u, int count, int extra) {
   return u <= 0 ? 0 : u <= extra + 1 ? 1 : u - extra < count ? (int)(u - extra) : count;
 }
-// The line of the units of all tiles and segments, cut into `warps` pieces:
-// `more` of q + 1 units, then the others of q.
+// A line of units cut into `warps` pieces: `more` of q + 1 units, then the
+// others of q.
 struct Line {
   int64_t q;
-  int warps, more, extra;
+  int warps, more;
 };
-FWPKM_HD Line cache_line(int64_t tiles, int64_t segments, int most) {
+FWPKM_HD Line cut_line(int64_t units, int warps) {
   Line l;
-  l.extra = tiles <= most ? 0 : 2;
-  const int64_t total = tiles + l.extra * segments;
-  const int64_t w = total / (l.extra ? l.extra + 2 : 1);  // smaller pieces are not worth a warp
-  l.warps = w < most ? (int)w : most;
-  l.q = total / l.warps;
-  l.more = (int)(total - l.q * l.warps);
+  l.warps = warps;
+  l.q = units / warps;
+  l.more = (int)(units - l.q * warps);
   return l;
 }
-// First unit of warp w's piece (w == warps: the end of the line).
+// First unit of piece w (w == warps: the end of the line).
 FWPKM_HD int64_t line_cut(const Line &l, int w) { return l.q * w + (w < l.more ? w : l.more); }
-// The warp whose piece holds a unit.
+// The piece that holds a unit.
 FWPKM_HD int line_owner(const Line &l, int64_t unit) {
   const int64_t big = (l.q + 1) * l.more;
   return unit < big ? (int)(unit / (l.q + 1)) : l.more + (int)((unit - big) / l.q);
 }
-// Warps of a CTA that take pieces: few pieces are spread over the CTAs, but not
-// thinner than `least` to a CTA, whose sums join in shared memory.
-FWPKM_HD int line_per_cta(const Line &l, int ctas, int least) {
-  const int n = (l.warps + ctas - 1) / ctas;
-  return n < least ? least : n;
+// The line in pieces for at most `most` warps, none of them too small to be
+// worth one (nor, with units beside the tiles, without a tile).
+FWPKM_HD Line piece_line(int64_t units, int most, int extra) {
+  const int64_t w = units / (extra ? extra + 2 : 1);
+  return cut_line(units, w < 1 ? 1 : w < most ? (int)w : most);
 }
+FWPKM_HD int extra_units(int64_t tiles, int most) { return tiles <= most ? 0 : 2; }
 
 }  // namespace fwpkm

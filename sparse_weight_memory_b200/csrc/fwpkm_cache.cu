@@ -264,6 +264,8 @@ extern "C" fwpkm_status fwpkm_cache_attend(const fwpkm_cache *cache,
   a.group = heads / a.p.kv_heads;
   a.window = window;
   a.div = page_div(a.p.page_size);
+  a.tokens = (int64_t)a.s.table_width * a.p.page_size;
+  if (window > 0 && window < a.tokens) a.tokens = window;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->dtype == FWPKM_F32    ? launch_cache_attend_f32(a, st)
                         : cache->dtype == FWPKM_BF16 ? launch_cache_attend_bf16(a, st)

@@ -67,6 +67,8 @@ struct AttendArgs {
   float scale_log2;  // scale * log2(e)
   int heads, group, blocks;  // group: query heads of a cached head, in `blocks` segments
   int window;
+  int64_t tokens;  // no sequence has more visible ones
+  int aligned;     // segments are short: none is divided between CTAs
   PageDiv div;  // by the page size
 };
 cudaError_t launch_cache_attend_bf16(const AttendArgs &a, cudaStream_t st);

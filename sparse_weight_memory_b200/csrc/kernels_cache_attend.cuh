@@ -35,7 +35,8 @@ namespace attend {
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLeastFactor = 1.18e-38f;  // a factor that no score feels, but not 0
-// Warps of a CTA that take pieces, at the least (where it has so many).
+// Warps of a CTA that take pieces, at the least (where it has so many): the
+// sums of those join in shared memory.
 constexpr int kLeastPerCta = 8;
 // A score may exceed the reference by this (base 2) before the sums are scaled
 // to a new one: weights stay under 2^(kShift + kSlack).
@@ -809,44 +810,75 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
     __syncthreads();
   }
   const Lengths lengths{a, kept, WARPS * 32};
-  const Line line = cache_line(before[WARPS * 32], (long long)a.s.B * hrs, gridDim.x * WARPS);
-  const int per = line_per_cta(line, gridDim.x, kLeastPerCta);  // pieces of a CTA
-  static_assert(kLeastPerCta <= WARPS, "no more than it has");
-  const long long seq_extra = (long long)line.extra * hrs;  // of a sequence's segments
+  const long long tiles = before[WARPS * 32];
+  const int extra = extra_units(tiles, gridDim.x * WARPS);
+  const long long total = tiles + (long long)extra * a.s.B * hrs;
+  // The segment that unit u < total falls into: its cursor, at tile 0.
+  auto find = [&](long long u) {
+    const long long seq_extra = (long long)extra * hrs;  // of a sequence's segments
+    // the thread whose sequences u falls into: the last one with so many before it
+    auto units = [&](int i) { return before[i] + seq_extra * min(i * chunk, a.s.B); };
+    int i = 0;
+    if (WARPS > 1) i = __popc(__ballot_sync(FULL, lane < WARPS && units(lane * 32) <= u)) - 1;
+    i = i * 32 + __popc(__ballot_sync(FULL, units(i * 32 + lane) <= u)) - 1;
+    Cursor c{};
+    long long p = units(i);
+    c.b = i * chunk;
+    c.enter(lengths, TT);
+    while (p + (long long)c.s.count * hrs + seq_extra <= u) {
+      p += (long long)c.s.count * hrs + seq_extra;
+      ++c.b;
+      c.enter(lengths, TT);
+    }
+    const long long n = c.s.count + extra;
+    c.hr = (int)((u - p) / n);
+    c.seg = p + c.hr * n;
+    return c;
+  };
+  // The line: of all units, its pieces dealt to the warps of all CTAs, or of the
+  // CTA's own segments.  Piece 0 of it is that of warp `shift`; the first unit
+  // is `base`.
+  Line line;
+  int per, shift;
+  long long base;
+  if (a.aligned) {
+    const Line share = cut_line(total, gridDim.x);
+    auto next_start = [&](long long u) {  // the first segment's start from unit u on
+      if (u >= total) return total;
+      const Cursor c = find(u);
+      return c.seg == u ? u : c.seg + c.s.count + extra;
+    };
+    base = next_start(line_cut(share, blockIdx.x));
+    const long long n = next_start(line_cut(share, blockIdx.x + 1)) - base;
+    line = n > 0 ? piece_line(n, WARPS, extra) : Line{};
+    per = WARPS;
+    shift = blockIdx.x * WARPS;
+  } else {
+    line = piece_line(total, gridDim.x * WARPS, extra);
+    per = max((line.warps + (int)gridDim.x - 1) / (int)gridDim.x, min(kLeastPerCta, WARPS));
+    shift = 0;
+    base = 0;
+  }
   const int w0 = blockIdx.x * per, w = w0 + warp;
-  const bool busy = warp < per && w < line.warps;
-  const long long u0 = busy ? line_cut(line, w) : 0;
-  const long long u1 = busy ? line_cut(line, w + 1) : 0;
+  const bool busy = warp < per && w - shift < line.warps;
+  const long long u0 = busy ? base + line_cut(line, w - shift) : 0;
+  const long long u1 = busy ? base + line_cut(line, w - shift + 1) : 0;
+  auto owner = [&](long long unit) { return line_owner(line, unit - base) + shift; };
 
   Cursor at{};  // the tile that is computed; at.left == 0: none is left
   if (busy) {
-    // the thread whose sequences u0 falls into: the last one with so many before it
-    auto units = [&](int i) { return before[i] + seq_extra * min(i * chunk, a.s.B); };
-    int i = 0;
-    if (WARPS > 1) i = __popc(__ballot_sync(FULL, lane < WARPS && units(lane * 32) <= u0)) - 1;
-    i = i * 32 + __popc(__ballot_sync(FULL, units(i * 32 + lane) <= u0)) - 1;
-    long long p = units(i);
-    at.b = i * chunk;
-    at.enter(lengths, TT);
-    while (p + (long long)at.s.count * hrs + seq_extra <= u0) {
-      p += (long long)at.s.count * hrs + seq_extra;
-      ++at.b;
-      at.enter(lengths, TT);
-    }
-    const long long n = at.s.count + line.extra;
-    at.hr = (int)((u0 - p) / n);
-    at.seg = p + at.hr * n;
-    at.tile = tile_from(u0 - at.seg, line.extra);
-    at.left = tiles_before(u1 - at.seg, at.s.count, line.extra) - at.tile;
-    if (at.tile >= at.s.count) at.next_segment(lengths, TT, u1, line.extra);  // behind its last
+    at = find(u0);
+    at.tile = tile_from(u0 - at.seg, extra);
+    at.left = tiles_before(u1 - at.seg, at.s.count, extra) - at.tile;
+    if (at.tile >= at.s.count) at.next_segment(lengths, TT, u1, extra);  // behind its last
   }
 
   // the segment that the CTA's first warp is in the middle of: k_join's CTAs share it
   if (threadIdx.x == 0) {
     int4 id = make_int4(0, 0, -1, 0);
     if (at.left > 0 && at.tile > 0)
-      id = make_int4(at.b, at.hr, line_owner(line, at.seg + tile_unit(at.s.count - 1, line.extra)),
-                     line_owner(line, at.seg));
+      id = make_int4(at.b, at.hr, owner(at.seg + tile_unit(at.s.count - 1, extra)),
+                     owner(at.seg));
     a.middles[blockIdx.x] = id;
   }
 
@@ -889,7 +921,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
       // the next tile's pages are looked up while this one's values are loaded
       ++ld.tile;
       if (--ld.left == 0 && ld.tile == ld.s.count)
-        ld.next_segment(lengths, TT, u1, line.extra);
+        ld.next_segment(lengths, TT, u1, extra);
       if (ld.left > 0) look();
     }
     if (even && packed) {
@@ -976,7 +1008,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
         const bool end = at.tile == count;
         seg = at.seg;
         if (end) {
-          at.next_segment(lengths, TT, u1, line.extra);
+          at.next_segment(lengths, TT, u1, extra);
           if (whole) {
             const int64_t r = first_row(b, hr);
             ty.finish(reinterpret_cast<Out *>(a.out) + r * a.p.dim, a.lse ? a.lse + r : nullptr,
@@ -992,7 +1024,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
           }
         }
         if (at.left == 0 && open) {  // what is left is joined with the CTA's other warps'
-          const int last = line_owner(line, seg + tile_unit(count - 1, line.extra));
+          const int last = owner(seg + tile_unit(count - 1, extra));
           if (lane == 0) last_at[warp] = make_int4(b, hr, last, whole);
           if (whole && !end) tail = make_int4(b, hr, last, 0);
         }
@@ -1260,9 +1292,11 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
   if (s.warps != WARPS || s.heads != TY::HEADS || s.part != TY::kParts * 128)
     return cudaErrorInvalidConfiguration;  // the workspace has another layout
   a.blocks = (a.group + TY::HEADS - 1) / TY::HEADS;
+  a.aligned = a.tokens / TY::TT + 2 <= 4 * WARPS;
   e = launch_k(true, k_attend<TY, WARPS, UNITS>, dim3(kAttendCtas), dim3(WARPS * 32),
                Layout<TY, WARPS, UNITS>::kSmem, st, a);
   if (e != cudaSuccess) return e;
+  if (a.aligned) return cudaSuccess;  // each CTA finishes its segments
   return launch_k(true, k_join<TY, WARPS>, dim3(kAttendCtas), dim3(kJoinWarps * 32), 0,
                   st, a);
 }

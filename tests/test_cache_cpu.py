@@ -28,15 +28,13 @@ void span(int len, int window, int tile, int *o) {
   Span s = cache_span(len, window, tile);
   o[0] = s.lo; o[1] = s.len; o[2] = s.first; o[3] = s.count;
 }
-void line(int64_t tiles, int64_t segments, int most, int ctas, int least, int64_t *o) {
-  Line l = cache_line(tiles, segments, most);
-  o[0] = l.warps; o[1] = l.extra; o[2] = line_per_cta(l, ctas, least);
+int extra_of(int64_t tiles, int most) { return extra_units(tiles, most); }
+int warps(int64_t units, int most, int extra) { return piece_line(units, most, extra).warps; }
+int64_t cut(int64_t units, int most, int extra, int w) {
+  return line_cut(piece_line(units, most, extra), w);
 }
-int64_t cut(int64_t tiles, int64_t segments, int most, int w) {
-  return line_cut(cache_line(tiles, segments, most), w);
-}
-int owner(int64_t tiles, int64_t segments, int most, int64_t unit) {
-  return line_owner(cache_line(tiles, segments, most), unit);
+int owner(int64_t units, int most, int extra, int64_t unit) {
+  return line_owner(piece_line(units, most, extra), unit);
 }
 int64_t unit_of(int j, int extra) { return tile_unit(j, extra); }
 int from(int64_t u, int extra) { return tile_from(u, extra); }
@@ -61,8 +59,8 @@ def sched(tmp_path_factory):
                     "-static-libubsan", "-shared", "-fPIC", "-I", fwbuild.CSRC,
                     str(d / "shim.cpp"), "-o", so], check=True)
     L = ctypes.CDLL(so)
-    L.line.argtypes = [i64, i64, i32, i32, i32, ctypes.POINTER(i64)]
-    L.cut.argtypes, L.owner.argtypes = [i64, i64, i32, i32], [i64, i64, i32, i64]
+    L.extra_of.argtypes, L.warps.argtypes = [i64, i32], [i64, i32, i32]
+    L.cut.argtypes, L.owner.argtypes = [i64, i32, i32, i32], [i64, i32, i32, i64]
     L.unit_of.argtypes, L.from_ = [i32, i32], getattr(L, "from")
     L.from_.argtypes, L.tiles.argtypes = [i64, i32], [i64, i32, i32]
     L.cut.restype = L.unit_of.restype = i64
@@ -95,20 +93,17 @@ def test_pieces_share_the_line_out(sched):
     most; and a segment's parts are those of its first warp to its last, none
     of them without a tile."""
     rng = np.random.default_rng(0)
-    o = (i64 * 3)()
     seen = set()
     for _ in range(200):
-        most = int(rng.choice([1, 5, 592, 1184, 2368]))
+        most = int(rng.choice([1, 5, 8, 16, 592, 1184, 2368]))
         big = int(np.exp(rng.uniform(0, np.log(3000))))
         counts = [int(c) for c in rng.integers(1, big + 1, int(rng.integers(1, 60)))]
-        line = (sum(counts), len(counts), most)
-        ctas = -(-most // 16)
-        sched.line(*line, ctas, 8, o)
-        n, extra, per = list(o)
+        extra = sched.extra_of(sum(counts), most)
         seen.add(extra)
-        assert extra == (0 if line[0] <= most else 2)
-        assert per * ctas >= n and per <= max(8, -(-most // ctas))
+        assert extra == (0 if sum(counts) <= most else 2)
         at = np.cumsum([0] + [c + extra for c in counts])
+        line = (int(at[-1]), most, extra)
+        n = sched.warps(*line)
         cuts = [sched.cut(*line, w) for w in range(n + 1)]
         sizes = np.diff(cuts)
         assert 1 <= n <= most and cuts[0] == 0 and cuts[-1] == at[-1]
@@ -129,8 +124,8 @@ def test_pieces_share_the_line_out(sched):
 
 
 def test_largest_line_stays_within_64_bits(sched):
-    line = ((1 << 22) * (1 << 28), 1 << 22, 2368)  # B * heads segments of 2^31 tokens
-    total = line[0] + 2 * line[1]
+    total = (1 << 22) * ((1 << 28) + 2)  # B * heads segments of 2^31 tokens
+    line = (total, 2368, 2)
     assert sched.cut(*line, 2368) == total
     assert sched.owner(*line, total - 1) == 2367
     assert sched.owner(*line, 0) == 0

@@ -160,6 +160,10 @@ def test_attend(dtype, heads, kv, dim, page):
     q = (2 * torch.randn((len(LENGTHS), heads, dim), generator=g, device="cuda")).to(
         F32 if dtype == F32 else BF)
     check(cache, q, table, LENGTHS)
+    # a table with room for longer sequences: the work is divided another way
+    wide = torch.full((len(LENGTHS), -(-9000 // page)), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    check(cache, q, wide, LENGTHS)
 
 
 @pytest.mark.parametrize("dtype", [BF, E4, F32])
