@@ -139,7 +139,7 @@ fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache, const fwpkm_cache_batc
  *   q         device [B][heads][dim], sequence b at element b*q_stride (a whole
  *             number of 16 bytes; 16-byte aligned); FWPKM_F32 for an F32 cache,
  *             FWPKM_BF16 for the others (FWPKM_EUNSUPPORTED otherwise)
- *   scale     finite; usually 1/sqrt(dim)
+ *   scale     finite, below 2e38 in size; usually 1/sqrt(dim)
  *   window    tokens visible before and including the newest, or 0: all
  *   out       device [B][heads][dim], q's type, 16-byte aligned
  *   lse       device fp32 [B][heads], or NULL

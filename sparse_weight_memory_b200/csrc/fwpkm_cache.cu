@@ -176,8 +176,9 @@ extern "C" fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache,
 fwpkm::AttendShape fwpkm::attend_shape(int cache_dtype, int dim, int group) {
   const int dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
   if (cache_dtype == FWPKM_F32) {
-    const int heads = group <= 4 ? 4 : 8;
-    return {dp == 64 ? 16 : dp == 128 ? 12 : 8, heads, heads * dp};
+    const int heads = group <= 4 ? 4 : group <= 8 || dp == 256 ? 8 : 16;
+    const int warps = heads == 16 || dp == 256 ? 8 : dp == 64 ? 16 : 12;
+    return {warps, heads, heads * dp};
   }
   const int heads = group <= 8 ? 8 : group <= 16 || dp == 256 ? 16 : 32;
   int warps = 16;
@@ -243,7 +244,9 @@ extern "C" fwpkm_status fwpkm_cache_attend(const fwpkm_cache *cache,
   if ((rc = check_rows(who, "q", q, q_stride, (int64_t)heads * a.p.dim, es, a.s.B))) return rc;
   if (!out || !aligned16(out))
     return fail(FWPKM_EINVAL, "%s: out must be given and 16-byte aligned", who);
-  if (!std::isfinite(scale)) return fail(FWPKM_EINVAL, "%s: scale must be finite", who);
+  const float scale_log2 = scale * 1.4426950408889634f;  // scores in base 2
+  if (!std::isfinite(scale_log2))
+    return fail(FWPKM_EINVAL, "%s: scale must be finite, and times log2(e) too", who);
   if (window < 0) return fail(FWPKM_EINVAL, "%s: window must be >= 0", who);
   const Workspace w = layout(cache->dtype, cache->dim, heads / cache->kv_heads);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < w.bytes)
@@ -259,7 +262,7 @@ extern "C" fwpkm_status fwpkm_cache_attend(const fwpkm_cache *cache,
   a.tails = reinterpret_cast<int4 *>(ws + w.tails);
   a.middles = reinterpret_cast<int4 *>(ws + w.middles);
   a.errors = device_errors;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.heads = heads;
   a.group = heads / a.p.kv_heads;
   a.window = window;

@@ -109,6 +109,17 @@ __device__ __forceinline__ unsigned transpose8(unsigned a) {  // of an 8 x 8 mat
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+// Two multiply-adds in one instruction, c += a * b, each rounded as fmaf does.
+struct alignas(8) Pair {
+  float x, y;
+};
+__device__ __forceinline__ void fma2(Pair &c, const Pair &a, const Pair &b) {
+  uint64_t cc = *reinterpret_cast<uint64_t *>(&c);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;"
+      : "+l"(cc)
+      : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
+  c = *reinterpret_cast<Pair *>(&cc);
+}
 // log sum e^s from a reference and a sum in base 2.
 __device__ __forceinline__ float log_sum(float m, float l) {
   return l == 0.f ? kNegInf : kLn2 * (m + log2f(l));
@@ -502,8 +513,8 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
 };
 
 // f32: the products run as plain 32-bit multiply-adds, which hold the full
-// accuracy; RR heads take RR of them an element, 8 flops a byte at 8 heads, a
-// third of what the SMs can do in the time of the bytes.  A group of LG lanes
+// accuracy, two to an instruction; RR heads take RR of them an element, 4 flops a
+// byte at 8 heads, a third of what the SMs can do in the time of the bytes.  A group of LG lanes
 // has two of the heads, a lane of it DP/LG elements of their queries and outputs
 // (in pieces of 4, the group's side by side).  A lane's sums of its elements, 8
 // tokens x 2 heads, are summed over the group by halving: each step exchanges
@@ -516,8 +527,8 @@ struct F32 {
   static constexpr int LG = 64 / RR, V4 = DP / LG / 4;  // lanes of a group, pieces of a lane
   static constexpr int NS = 16 / LG;                    // scores of a lane: tokens of one head
   static constexpr int kParts = 2 * V4, kQuery = 0;
-  static_assert(RR == 4 || RR == 8, "groups of 16 or 8 lanes");
-  float q[2][V4][4], o[2][V4][4];
+  static_assert(RR == 4 || RR == 8 || RR == 16, "groups of 16, 8 or 4 lanes");
+  Pair q[2][V4][2], o[2][V4][2];  // element pairs
   float c, m, l;  // of head head(); l: of the lane's own tokens
   float p[NS];
   int dim;
@@ -536,7 +547,7 @@ struct F32 {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < V4; ++i) o[h][i][0] = o[h][i][1] = o[h][i][2] = o[h][i][3] = 0.f;
+      for (int i = 0; i < V4; ++i) o[h][i][0] = o[h][i][1] = Pair{0.f, 0.f};
   }
   __device__ __forceinline__ void load_q(const char *qp, int rows, int dim_, float f) {
     dim = dim_;
@@ -549,35 +560,39 @@ struct F32 {
         if (row < rows && e < dim)
           v = __ldg(reinterpret_cast<const float4 *>(qp + (row * dim + e) * 4));
         const float sign = f < 0.f ? -1.f : 1.f;
-        q[h][i][0] = v.x * sign;
-        q[h][i][1] = v.y * sign;
-        q[h][i][2] = v.z * sign;
-        q[h][i][3] = v.w * sign;
+        q[h][i][0] = Pair{v.x * sign, v.y * sign};
+        q[h][i][1] = Pair{v.z * sign, v.w * sign};
       }
     c = fmaxf(fabsf(f), kLeastFactor);
   }
-  __device__ __forceinline__ static void lds4(float (&x)[4], const char *a) {
+  __device__ __forceinline__ static void lds4(Pair (&x)[2], const char *a) {
     const float4 v = *reinterpret_cast<const float4 *>(a);
-    x[0] = v.x;
-    x[1] = v.y;
-    x[2] = v.z;
-    x[3] = v.w;
+    x[0] = Pair{v.x, v.y};
+    x[1] = Pair{v.z, v.w};
   }
   __device__ __forceinline__ void scores(const char *ks, unsigned vis) {
     const char *a0 = ks + lane() % LG * 16;
-    float x[16] = {};
+    float x[16];
 #pragma unroll
-    for (int i = 0; i < V4; ++i) {
-      if (i * LG * 4 >= dim) break;  // (only zeros from here on)
+    for (int t0 = 0; t0 < 8; t0 += 4) {  // (four tokens' pairs of sums at a time)
+      Pair sum[2][4] = {};
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        float k[4];
-        lds4(k, a0 + t * PITCH + i * LG * 16);
+      for (int i = 0; i < V4; ++i) {
+        if (i * LG * 4 >= dim) break;  // (only zeros from here on)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int t = 0; t < 4; ++t) {
+          Pair k[2];
+          lds4(k, a0 + (t0 + t) * PITCH + i * LG * 16);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[h * 8 + t] = fmaf(q[h][i][e], k[e], x[h * 8 + t]);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) fma2(sum[h][t], q[h][i][e], k[e]);
+        }
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x[h * 8 + t0 + t] = sum[h][t].x + sum[h][t].y;
     }
 #pragma unroll
     for (int w = LG / 2, n = 8; w > 0; w >>= 1, n >>= 1) {
@@ -607,7 +622,7 @@ struct F32 {
 #pragma unroll
         for (int i = 0; i < V4; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[h][i][e] *= fh;
+          for (int e = 0; e < 2; ++e) o[h][i][e] = Pair{o[h][i][e].x * fh, o[h][i][e].y * fh};
       }
     }
     const float u = m == kNegInf ? 0.f : m;
@@ -629,12 +644,12 @@ struct F32 {
       if (i * LG * 4 >= dim) break;
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        float v[4];
+        Pair v[2];
         lds4(v, a0 + t * PITCH + i * LG * 16);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[h][i][e] = fmaf(w[h][t], v[e], o[h][i][e]);
+          for (int e = 0; e < 2; ++e) fma2(o[h][i][e], Pair{w[h][t], w[h][t]}, v[e]);
       }
     }
   }
@@ -643,8 +658,8 @@ struct F32 {
     for (int w = 4 / NS; w > 0; w >>= 1) l += __shfl_xor_sync(FULL, l, w);
   }
   __device__ __forceinline__ float4 part(int i) const {
-    const float(&x)[4] = o[i / V4][i % V4];
-    return make_float4(x[0], x[1], x[2], x[3]);
+    const Pair(&x)[2] = o[i / V4][i % V4];
+    return make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
   }
   template <typename F>
   __device__ __forceinline__ void stats(F &&f) const {
@@ -666,7 +681,7 @@ struct F32 {
         const int e = (i * LG + lane() % LG) * 4;
         if (row < rows && e < dim)
           *reinterpret_cast<float4 *>(out + row * dim + e) =
-              make_float4(o[h][i][0] * f, o[h][i][1] * f, o[h][i][2] * f, o[h][i][3] * f);
+              make_float4(o[h][i][0].x * f, o[h][i][0].y * f, o[h][i][1].x * f, o[h][i][1].y * f);
       }
     }
     if (lse)

@@ -253,7 +253,8 @@ def test_append_refusals(lib, kw, status):
     (dict(q_dtype=2), FWPKM_EINVAL), (dict(q_dtype=FWPKM_F32), FWPKM_EUNSUPPORTED),
     (dict(q=None), FWPKM_EINVAL), (dict(q_stride=1016), FWPKM_ESHAPE), (dict(out=None), FWPKM_EINVAL),
     (dict(out=FAKE + 4), FWPKM_EINVAL), (dict(scale=float("nan")), FWPKM_EINVAL),
-    (dict(scale=float("inf")), FWPKM_EINVAL), (dict(window=-1), FWPKM_EINVAL),
+    (dict(scale=float("inf")), FWPKM_EINVAL), (dict(scale=3e38), FWPKM_EINVAL),
+    (dict(window=-1), FWPKM_EINVAL),
     (dict(workspace=None), FWPKM_EINVAL), (dict(workspace=FAKE + 16), FWPKM_EINVAL),
     (dict(workspace_bytes=1000), FWPKM_EINVAL),
 ])

@@ -363,6 +363,12 @@ def test_attend_equal_bits_and_streams():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+    # a workspace of the caller's, whatever it holds
+    size = cache.attend_workspace(6, 8)
+    for fill in (0, 255):
+        own = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            assert torch.equal(cache.attend(qs[0], table, lens, workspace=own), want[0])
     # a captured call follows new lengths, tables and queries
     graphs, outs = [], []
     q = qs[0].clone()
