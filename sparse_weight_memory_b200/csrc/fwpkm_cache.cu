@@ -176,8 +176,8 @@ extern "C" fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache,
 // times as long (e4m3 heads of 256 on 12 warps 507 us, on 8 150).  Measured on 2 M
 // tokens and alike: bf16 heads of 128 on 8, 10, 12 and 16 warps 192, 191, 185 and
 // 192 us, e4m3 143, 151, 150 and 157, bf16 heads of 64 147, 147, 142 and 142.
-// More than 8 query heads to a cached one are one segment of 16 or 32: in
-// segments of 16, 32 heads read the cache twice (567 us where 228).
+// More than 8 query heads to a cached one are one segment of 16 or 32, since every
+// further segment reads the cached head again.
 fwpkm::AttendShape fwpkm::attend_shape(int cache_dtype, int dim, int group) {
   const int dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
   if (cache_dtype == FWPKM_F32) {
