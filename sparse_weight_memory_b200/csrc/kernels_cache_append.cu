@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(256, 2)
   griddep_launch();
   const int lanes = lanes_of(a);
   const int64_t n = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (n >= (int64_t)a.rows * lanes) return;
   const int row = (int)(n / lanes), i = (int)(n - (int64_t)row * lanes);
-  if (row >= a.rows) return;
   const int all = a.heads + 2 * a.p.kv_heads, rotated = a.heads + a.p.kv_heads;
   const Item turned = item_of(a, i, false), copied = item_of(a, i, true);
   Raw<TI> x[kBatch], y[kBatch];
