@@ -131,7 +131,9 @@ fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache, const fwpkm_cache_batc
  *   out = sum_t softmax(s)_t v_t,   lse = log sum_t exp(s_t),
  * with lo = max(0, lengths[b] - window), or 0 where window is 0; query head i
  * reads cached head i / (heads / kv_heads).  A sequence without visible tokens
- * gives out = 0 and lse = -infinity.  Scores, softmax and sums are held in 32
+ * gives out = 0 and lse = -infinity, and so does a head whose visible scores are
+ * all -infinity; a NaN or +infinity among a head's visible scores makes that
+ * sequence's head NaN, and no other.  Scores, softmax and sums are held in 32
  * bits, out is rounded once.  What lies in the pool outside the visible tokens
  * does not matter, infinities and NaN included.  The result does not depend on
  * timing: equal calls give equal bits.
@@ -141,7 +143,8 @@ fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache, const fwpkm_cache_batc
  *             FWPKM_BF16 for the others (FWPKM_EUNSUPPORTED otherwise)
  *   scale     finite, below 2e38 in size; usually 1/sqrt(dim)
  *   window    tokens visible before and including the newest, or 0: all
- *   out       device [B][heads][dim], q's type, 16-byte aligned
+ *   out       device [B][heads][dim], q's type, 16-byte aligned; like lse, it
+ *             overlaps no input (q least of all)
  *   lse       device fp32 [B][heads], or NULL
  *   workspace device memory of at least fwpkm_cache_attend_workspace(...)
  *             bytes, 256-byte aligned, for this call alone until it has run;

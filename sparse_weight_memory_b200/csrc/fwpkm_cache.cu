@@ -249,6 +249,7 @@ extern "C" fwpkm_status fwpkm_cache_attend(const fwpkm_cache *cache,
   if ((rc = check_rows(who, "q", q, q_stride, (int64_t)heads * a.p.dim, es, a.s.B))) return rc;
   if (!out || !aligned16(out))
     return fail(FWPKM_EINVAL, "%s: out must be given and 16-byte aligned", who);
+  if (out == q) return fail(FWPKM_EINVAL, "%s: out must not be q", who);
   const float scale_log2 = scale * 1.4426950408889634f;  // scores in base 2
   if (!std::isfinite(scale_log2))
     return fail(FWPKM_EINVAL, "%s: scale must be finite, and times log2(e) too", who);

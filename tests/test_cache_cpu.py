@@ -193,7 +193,7 @@ def batch(**kw):
 APPEND = dict(rows=2, in_dtype=FWPKM_BF16, k=FAKE, k_stride=512, v=FAKE, v_stride=512, q=FAKE,
               q_stride=1024, q_out=2 * FAKE, q_out_stride=1024, heads=16, starts=None, rotary=64,
               style=0, freqs=FAKE, errors=None, stream=None)
-ATTEND = dict(heads=16, q_dtype=FWPKM_BF16, q=FAKE, q_stride=1024, scale=0.125, window=0, out=FAKE,
+ATTEND = dict(heads=16, q_dtype=FWPKM_BF16, q=FAKE, q_stride=1024, scale=0.125, window=0, out=2 * FAKE,
               lse=None, workspace=FAKE, workspace_bytes=1 << 40, errors=None, stream=None)
 
 
@@ -252,7 +252,7 @@ def test_append_refusals(lib, kw, status):
     (dict(heads=12), FWPKM_ESHAPE), (dict(heads=0), FWPKM_ESHAPE), (dict(heads=8192), FWPKM_ESHAPE),
     (dict(q_dtype=2), FWPKM_EINVAL), (dict(q_dtype=FWPKM_F32), FWPKM_EUNSUPPORTED),
     (dict(q=None), FWPKM_EINVAL), (dict(q_stride=1016), FWPKM_ESHAPE), (dict(out=None), FWPKM_EINVAL),
-    (dict(out=FAKE + 4), FWPKM_EINVAL), (dict(scale=float("nan")), FWPKM_EINVAL),
+    (dict(out=FAKE + 4), FWPKM_EINVAL), (dict(out=FAKE, q=FAKE), FWPKM_EINVAL), (dict(scale=float("nan")), FWPKM_EINVAL),
     (dict(scale=float("inf")), FWPKM_EINVAL), (dict(scale=3e38), FWPKM_EINVAL),
     (dict(window=-1), FWPKM_EINVAL),
     (dict(workspace=None), FWPKM_EINVAL), (dict(workspace=FAKE + 16), FWPKM_EINVAL),

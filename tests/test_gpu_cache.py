@@ -2,14 +2,13 @@
 
 Tolerances.  A result rounded to type T is off by half a step, u = eps(T)/2 of
 it.  What the kernels add before that rounding:
-  - a score is a sum of dim products held in 32 bits (products of two TF32
-    parts leave 2^-22 of a term): ds <= scale * sum |q_i k_i| * (dim + 16) 2^-23,
-    and for 8-bit caches scale * max |q| * sum |k_i| * 2^-25 more (queries in
+  - a score is a sum of dim products held in 32 bits:
+    ds <= scale * sum |q_i k_i| * (dim + 16) 2^-23, and for 8-bit caches scale * max |q| * sum |k_i| * 2^-25 more (queries in
     16-bit floats);
   - a weight 2^(s-m) is then off by ds (its exponent) and 2^-22 (exp2), twice
     (numerator and denominator); as an operand of the second product it is
-    rounded to two bf16 parts (2^-16), to 11 bits (2^-11, 8-bit caches) or to
-    two TF32 parts (2^-22);
+    rounded to two bf16 parts (2^-16), to 11 bits (2^-11, 8-bit caches) or, in
+    32 bits, not at all (2^-22 is given it);
   - the sums over n tokens run in 32 bits in n/8 steps and a join: (n/8 + 64) 2^-23.
 An output is off by these shares of sum_t p_t |v_t|.  lse is off by ds, the
 sums' share and the roundings of ln 2 (m + log2 l): 4 * 2^-23 (|lse| + |m|).
@@ -279,6 +278,48 @@ def test_attend_peaked_scores(dtype):
             cache.keys[at] = row.to(dtype)
     for scale in (None, 1.0, 0.0, -0.3):
         check(cache, q, table, lengths, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, E4, F32])
+def test_attend_keeps_a_bad_score_to_its_head(dtype):
+    """A NaN among the visible keys or values reaches its sequence's head (its
+    element) and nothing else, bit for bit; a head whose scores are all -infinity
+    has none to weigh."""
+    g = gen(14)
+    lengths = [5000, 1, 0, 700, 9000, 33]
+    table, pages = make_table(g, lengths, 32)
+    cache = make_pool(g, pages, 2, 32, 128, dtype)
+    q = torch.randn((6, 8, 128), generator=g, device="cuda").to(F32 if dtype == F32 else BF)
+    q[5, :, 0] = 1
+    lens = as_int32(lengths)
+
+    def attend():
+        lse = torch.empty((6, 8), device="cuda")
+        return cache.attend(q, table, lens, lse=lse), lse
+
+    def put(pool, b, t, h, e, x):  # element by element: fp8 has no indexed fill
+        row = pool[table[b][t // 32].item(), h, t % 32]
+        row[e:e + 1].copy_(torch.tensor([x], device="cuda").to(dtype))
+
+    want, want_lse = attend()
+    put(cache.keys, 3, 111, 1, 7, math.nan)
+    put(cache.values, 4, 8000, 0, 5, math.nan)
+    rest = torch.ones((6, 8, 128), dtype=torch.bool, device="cuda")
+    rest[3, 4:] = False
+    rest[4, :4, 5] = False
+    out, lse = attend()
+    assert torch.equal(out[rest], want[rest]) and out[~rest].isnan().all()
+    keep = torch.ones((6, 8), dtype=torch.bool, device="cuda")
+    keep[3, 4:] = False
+    assert torch.equal(lse[keep], want_lse[keep]) and lse[~keep].isnan().all()
+    if dtype == E4:
+        return  # the type has no infinity
+    for t in range(33):
+        put(cache.keys, 5, t, 1, 0, -math.inf)
+    rest[5, 4:] = False
+    out, lse = attend()
+    assert torch.equal(out[rest], want[rest])
+    assert (out[5, 4:] == 0).all() and (lse[5, 4:] == -math.inf).all()
 
 
 def test_attend_tiny_and_huge_queries():
