@@ -40,6 +40,7 @@ class _Batch(ctypes.Structure):  # fwpkm_cache_batch
                 ("table_stride", ctypes.c_int64), ("table", _vp), ("lengths", _vp)]
 
 
+_INT = 2 ** 31  # sizes from here on do not fit the library's ints
 _lib = None
 
 
@@ -85,6 +86,11 @@ class KVCache:
     Row b of ``table`` (int32 [B][width]) lists the pages of sequence b in
     order; ``lengths`` (int32 [B]) are the sequences' tokens, the new ones
     included.  Both lie on the device, so a captured graph follows them.
+
+    ``stream`` (a torch stream or a handle) is where a call runs, the current
+    one by default.  Tensors that the caller gives back before it has run there
+    need ``record_stream``, as for any work on a second stream.  No gradients
+    pass through either call.
     """
 
     def __init__(self, pages: Optional[int] = None, page_size: Optional[int] = None,
@@ -107,6 +113,7 @@ class KVCache:
                "keys and values must be [pages][kv_heads][page_size][dim]")
         _shape(keys.stride(3) == 1 and keys.stride() == values.stride(),
                "keys and values need a contiguous last dimension and the same strides")
+        _shape(max(keys.shape) < _INT, "a cache's sizes must be under 2^31")
         self._keys, self._values = keys, values
         self._scales = (key_scale, value_scale)
         self.device, self.dtype = keys.device, keys.dtype
@@ -159,6 +166,8 @@ class KVCache:
             raise FwpkmError(FWPKM_ESHAPE, "table must be [B][width] and lengths [B], B and width "
                              ">= 1")
         B, width = shape
+        if B >= _INT or width >= _INT:
+            raise FwpkmError(FWPKM_ESHAPE, "table's sizes must be under 2^31")
         rows, cols = table.stride()
         if (cols != 1 and width > 1) or (rows < width and B > 1):
             raise FwpkmError(FWPKM_ESHAPE, "table rows must be contiguous")
@@ -173,6 +182,8 @@ class KVCache:
                 (heads is not None and shape[1] != heads):
             raise FwpkmError(FWPKM_ESHAPE, f"{name} must be [{rows}]"
                              f"[{'heads' if heads is None else heads}][{dim}]")
+        if rows >= _INT or shape[1] >= _INT:
+            raise FwpkmError(FWPKM_ESHAPE, f"{name}'s sizes must be under 2^31")
         step, head, one = t.stride()
         if one != 1 or (head != dim and shape[1] > 1):
             raise FwpkmError(FWPKM_ESHAPE, f"the rows of {name} must be contiguous")
@@ -200,6 +211,9 @@ class KVCache:
             else:
                 if not isinstance(stream, torch.cuda.Stream):
                     stream = torch.cuda.ExternalStream(stream or 0, device=self.device)
+                elif stream.device != self.device:
+                    raise FwpkmError(FWPKM_EINVAL, f"a stream of {stream.device}, a cache on "
+                                     f"{self.device}")
                 with torch.cuda.stream(stream):
                     yield
 
@@ -275,6 +289,8 @@ class KVCache:
 
     def _attend(self, q, table, lengths, scale, window, out, lse, errors, workspace):
         batch = self._batch(table, lengths)
+        if not 0 <= window < _INT:
+            raise FwpkmError(FWPKM_EINVAL, f"window={window} must be 0 .. 2^31 - 1")
         dtype, B = q.dtype, batch.B
         if dtype not in _INPUTS:
             raise TypeError(f"unsupported dtype {dtype}")

@@ -2,6 +2,7 @@
 places of new tokens (cache_schedule.cuh compiled for the host), the refusals
 of both calls, and the binding's constants."""
 import ctypes
+import functools
 import os
 import re
 import subprocess
@@ -359,6 +360,27 @@ def test_binding_refuses_attend(lib, kw, error):
 def test_binding_refuses_caches(lib, kw, error):
     with pytest.raises(error):
         cpu_cache(**kw)
+
+
+def test_binding_refuses_sizes_beyond_an_int(lib):
+    """Sizes and windows that would wrap around on their way into the library (tensors
+    without storage stand in for the large ones)."""
+    bf, far = torch.bfloat16, 2**32 + 2
+    empty = functools.partial(torch.empty, device="meta")
+    long = dict(k=empty(far, 2, 64, dtype=bf), v=empty(far, 2, 64, dtype=bf), q=None)
+    many = dict(table=empty(far, 3, dtype=torch.int32), lengths=empty(far, dtype=torch.int32))
+    for kw in (long, many, dict(table=empty(2, far, dtype=torch.int32)),
+               dict(q=empty(2, far, 64, dtype=bf))):
+        with pytest.raises(FwpkmError, match="2\\^31"):
+            cpu_cache().append(**cpu_args(**kw))
+    for window in (-1, 2**31, far, -far):
+        a = cpu_args(window=window)
+        a.pop("k"), a.pop("v")
+        with pytest.raises(FwpkmError, match="window"):
+            cpu_cache().attend(**a)
+    pool = empty(4, 2, far, 64, dtype=bf)
+    with pytest.raises(FwpkmError, match="2\\^31"):
+        KVCache(keys=pool, values=pool)
 
 
 def test_pool_layouts(lib):
