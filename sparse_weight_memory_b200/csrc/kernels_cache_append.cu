@@ -141,23 +141,19 @@ __device__ __forceinline__ void rotate(float &u, float &z, const float2 &w) {
   z = fmaf(z, w.x, u0 * w.y);
 }
 
-// What a thread does of a row's head: 8 elements or, in a head rotated by
-// halves, two groups of 8 that turn together.  A query or key head has
-// lanes_of() such items, a value head is shared out over the same ones.
+// What a thread does of a row's head: two groups of 8 elements (one where their
+// number is odd), in a head rotated by halves two that turn together.  With one
+// group a thread behind the rotated elements, half the bytes were under way: 64
+// of 256 elements rotated took 112 us where all 256 took 63.
 struct Item {
   int c, c2;  // groups of 8; c2 may be -1
 };
-FWPKM_HD int lanes_of(const AppendArgs &a) {
-  return a.pairs ? a.p.dim / 8 : a.p.dim / 8 - a.rotary / 16;
-}
+FWPKM_HD int lanes_of(const AppendArgs &a) { return (a.p.dim + 8) / 16; }
 __device__ __forceinline__ Item item_of(const AppendArgs &a, int i, bool value) {
-  if (value) {
-    const int c2 = i + lanes_of(a);
-    return {i, c2 < a.p.dim / 8 ? c2 : -1};
-  }
-  if (a.pairs) return {i, -1};
-  const int H8 = a.rotary / 16;
-  return i < H8 ? Item{i, i + H8} : Item{i + H8, -1};  // rotated; behind the rotated elements
+  const int half = value || a.pairs ? 0 : a.rotary / 16;  // groups of half the rotated elements
+  if (i < half) return {i, i + half};
+  const int c = i + half, c2 = c + lanes_of(a) - half;  // behind them
+  return {c, c2 < a.p.dim / 8 ? c2 : -1};
 }
 // Heads of a row in the order queries, keys, values.
 template <typename TI>
@@ -237,11 +233,15 @@ __global__ void __launch_bounds__(kMaxThreads)
     if (m.c2 >= 0) z = unpack(y);
     if (h < rotated) {
       if (a.pairs) {
-        if (i < a.rotary / 8)
+        if (m.c < a.rotary / 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            rotate(u.x[2 * e], u.x[2 * e + 1], turn[row * half + i * 4 + e]);
-      } else if (m.c2 >= 0) {
+            rotate(u.x[2 * e], u.x[2 * e + 1], turn[row * half + m.c * 4 + e]);
+        if (m.c2 >= 0 && m.c2 < a.rotary / 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            rotate(z.x[2 * e], z.x[2 * e + 1], turn[row * half + m.c2 * 4 + e]);
+      } else if (i < a.rotary / 16) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) rotate(u.x[e], z.x[e], turn[row * half + i * 8 + e]);
       }
@@ -283,12 +283,18 @@ __global__ void __launch_bounds__(256, 2)
   int h0 = blockIdx.y;
   load(h0);
   const Place pl = find_place(a, row);
-  constexpr int kTurns = PAIRS ? 4 : 8;
-  const bool turns = PAIRS ? i < a.rotary / 8 : turned.c2 >= 0;
-  float2 w[kTurns];
+  // by halves: angles 8 i .. of both groups; by pairs: 4 of each group's own
+  const bool turns = PAIRS ? turned.c < a.rotary / 8 : i < a.rotary / 16;
+  const bool turns2 = PAIRS && turned.c2 >= 0 && turned.c2 < a.rotary / 8;
+  float2 w[8];
   if (turns)
 #pragma unroll
-    for (int e = 0; e < kTurns; ++e) w[e] = turn_of(max(pl.pos, 0), __ldg(a.freqs + i * kTurns + e));
+    for (int e = 0; e < (PAIRS ? 4 : 8); ++e)
+      w[e] = turn_of(max(pl.pos, 0), __ldg(a.freqs + i * (PAIRS ? 4 : 8) + e));
+  if (turns2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[4 + e] = turn_of(max(pl.pos, 0), __ldg(a.freqs + turned.c2 * 4 + e));
   while (true) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -299,10 +305,14 @@ __global__ void __launch_bounds__(256, 2)
       if (m.c2 >= 0) z = unpack(y[j]);
       if (h < rotated && turns) {
 #pragma unroll
-        for (int e = 0; e < kTurns; ++e) {
+        for (int e = 0; e < (PAIRS ? 4 : 8); ++e) {
           if (PAIRS) rotate(u.x[2 * (e % 4)], u.x[2 * (e % 4) + 1], w[e]);
           else rotate(u.x[e], z.x[e], w[e]);
         }
+      }
+      if (PAIRS && h < rotated && turns2) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rotate(z.x[2 * e], z.x[2 * e + 1], w[4 + e]);
       }
       put<TI, TC>(a, row, pl, h, m, u, z);
     }
