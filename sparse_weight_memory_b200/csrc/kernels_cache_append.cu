@@ -22,6 +22,8 @@ constexpr int kMaxRows = 8;  // rows of a CTA of k_append_few
 // rows of 48 heads of 128 (1024 items) take 5.0 us one way and 6.4 this way, 512
 // rows 8.5 and 6.4, 256 rows the same.
 constexpr int kManyThreads = 2048;
+template <typename TI>
+constexpr int kBatch = sizeof(TI) == 2 ? 6 : 3;  // heads that a thread of it loads at once
 constexpr int kMaxPairs = FWPKM_CACHE_MAX_DIM / 2;
 
 struct Eight {
@@ -250,28 +252,30 @@ __global__ void __launch_bounds__(kMaxThreads)
   }
 }
 
-// Many rows: a thread to an item of a row, for all of the row's heads or, with
-// several splits, a share of them.  Its angles are the same for all heads: they
-// stay in registers, each computed once, and no thread waits for another.
-// kBatch heads' elements are loaded at once.  19235 rows of 36 bf16 heads of 128
-// (354 MB) take 64 us, 85% of the measured copy rate; with the angles in shared
-// memory, shared by a CTA's threads behind barriers, they took 96.
+// Many rows: `splits` threads to an item of a row, each for every splits-th head.
+// The angles are the same for all heads: they stay in registers, and no thread
+// waits for another.  The splits of a row are neighbours, so that neighbouring
+// heads are read and written at about the same time: in CTAs of their own, the
+// same shares took 64 us instead of 50 at heads of 80.  19235 rows of 36 bf16
+// heads of 128 (354 MB) take 64 us, 85% of the measured copy rate; with the angles
+// in shared memory, shared by a CTA's threads behind barriers, they took 96.
 template <typename TI, typename TC, bool PAIRS>
 __global__ void __launch_bounds__(256, 2)
     k_append_many(const __grid_constant__ AppendArgs a, int splits) {
-  constexpr int kBatch = sizeof(TI) == 2 ? 6 : 3;
   griddep_wait();
   griddep_launch();
   const int lanes = lanes_of(a);
   const int64_t n = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (n >= (int64_t)a.rows * lanes) return;
-  const int row = (int)(n / lanes), i = (int)(n - (int64_t)row * lanes);
+  const int threads = lanes * splits;  // of a row
+  if (n >= (int64_t)a.rows * threads) return;
+  const int row = (int)(n / threads), split = (int)(n - (int64_t)row * threads) / lanes;
+  const int i = (int)(n - (int64_t)row * threads) - split * lanes;
   const int all = a.heads + 2 * a.p.kv_heads, rotated = a.heads + a.p.kv_heads;
   const Item turned = item_of(a, i, false), copied = item_of(a, i, true);
-  Raw<TI> x[kBatch], y[kBatch];
+  Raw<TI> x[kBatch<TI>], y[kBatch<TI>];
   auto load = [&](int h0) {
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
+    for (int j = 0; j < kBatch<TI>; ++j) {
       const int h = h0 + j * splits;
       if (h >= all) break;
       const Item m = h < rotated ? turned : copied;
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(256, 2)
       if (m.c2 >= 0) y[j] = load8(src + m.c2 * 8);
     }
   };
-  int h0 = blockIdx.y;
+  int h0 = split;
   load(h0);
   const Place pl = find_place(a, row);
   // by halves: angles 8 i .. of both groups; by pairs: 4 of each group's own
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(256, 2)
       w[4 + e] = turn_of(max(pl.pos, 0), __ldg(a.freqs + turned.c2 * 4 + e));
   while (true) {
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
+    for (int j = 0; j < kBatch<TI>; ++j) {
       const int h = h0 + j * splits;
       if (h >= all) break;
       const Item m = h < rotated ? turned : copied;
@@ -316,7 +320,7 @@ __global__ void __launch_bounds__(256, 2)
       }
       put<TI, TC>(a, row, pl, h, m, u, z);
     }
-    h0 += kBatch * splits;
+    h0 += kBatch<TI> * splits;
     if (h0 >= all) break;
     load(h0);
   }
@@ -328,18 +332,20 @@ cudaError_t launch(const AppendArgs &a, cudaStream_t st) {
   const int64_t threads = (int64_t)a.rows * lanes;
   if (threads >= kManyThreads) {
     // the splits of the heads that take the least time: rounds of two CTAs an
-    // SM, times the heads of a split and what its angles cost beside them
-    const int64_t ctas = (threads + 255) / 256;
+    // SM, times the heads of a split and what its angles cost beside them; two
+    // at the least where each has a batch of heads (19235 rows of 36 heads of 80:
+    // 60 us with one, 50 with two; of 3 heads of 128: 12.5 and 18.7)
+    auto ctas = [&](int n) { return (threads * n + 255) / 256; };
     int splits = 1;
     int64_t best = INT64_MAX;
-    for (int n = 1; n <= all && n <= 64; ++n) {
-      const int64_t time = (ctas * n + 295) / 296 * ((all + n - 1) / n + 8);
+    for (int n = all >= 2 * kBatch<TI> ? 2 : 1; n <= all && n <= 64; ++n) {
+      const int64_t time = (ctas(n) + 295) / 296 * ((all + n - 1) / n + 8);
       if (time < best) {
         best = time;
         splits = n;
       }
     }
-    const dim3 grid((unsigned)ctas, splits);
+    const dim3 grid((unsigned)ctas(splits));
     return a.pairs ? launch_k(true, k_append_many<TI, TC, true>, grid, dim3(256), 0, st, a, splits)
                    : launch_k(true, k_append_many<TI, TC, false>, grid, dim3(256), 0, st, a, splits);
   }
