@@ -511,6 +511,30 @@ def test_append(inputs, dtype, heads, kv, dim, page, rotary, style, layout):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("inputs,dtype", [(BF, BF), (F32, F32)])
+@pytest.mark.parametrize("style", ["halves", "pairs"])
+@pytest.mark.parametrize("dim,rotary", [(8, 0), (24, 16), (40, 16), (72, 64), (200, 112), (248, 48)])
+def test_append_odd_widths(inputs, dtype, style, dim, rotary):
+    """Heads of an odd number of 8-element groups, in part rotated, few rows and many."""
+    g = gen(dim)
+    heads, kv, page = 13, 2, 50
+    freqs = torch.rand(rotary // 2, generator=g, device="cuda") if rotary else None
+    for rows in (5, 2500):
+        cache = make_pool(g, 51, kv, page, dim, dtype)
+        table = torch.randperm(51, generator=g, device="cuda").int()[None]
+        qkv = torch.randn((rows, heads + 2 * kv, dim), generator=g, device="cuda").to(inputs)
+        q, k, v = qkv.split([heads, kv, kv], 1)
+        got = cache.append(k, v, table, as_int32([rows + 40]), starts=as_int32([0, rows]), q=q,
+                           freqs=freqs, style=style)
+        pos = torch.arange(40, rows + 40, device="cuda")
+        want, size = rotated(q, pos, freqs, style)
+        close(got, want, size, inputs)
+        pg, row = table[0][pos // page].long(), pos % page
+        want, size = rotated(k, pos, freqs, style)
+        close(cache.keys[pg, :, row], want, size, dtype)
+        assert torch.equal(cache.values[pg, :, row], v.to(dtype))
+
+
 @pytest.mark.parametrize("inputs,dtype", [(BF, BF), (BF, E4), (F32, F32)])
 @pytest.mark.parametrize("style", ["halves", "pairs"])
 def test_append_one_token_in_place(inputs, dtype, style):
