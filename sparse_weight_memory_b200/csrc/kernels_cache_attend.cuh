@@ -392,8 +392,12 @@ struct Bf16 : Mma<Bf16<DP_, TT_, NT_>, DP_, TT_, NT_> {
 // element lies in [1, 2): what a bf16 element then loses to the 16-bit range is
 // under 2^-25 of the largest, no more than the 32-bit sum.  Weights are held
 // 2^8 too large (kShift), which keeps all down to 2^-22 of the largest above
-// the 16-bit format's smallest normal number; at 11 bits their rounding is an
-// eighth of the result's.
+// the 16-bit format's smallest normal number, and go in as two parts, 22 bits: one
+// part alone, 11 bits, left errors of 2^-12 of the terms, which show where an
+// output is far smaller than they are.  With up to 8 heads to a cached one the
+// second product costs nothing (8 cached heads of 128 in 8 query heads each, 1.17
+// GB: 205 us with one, 200 with two); with 16 it takes 160 -> 178 us (heads of
+// 128, 0.78 GB) and 101 -> 112 (of 64, 0.39 GB).
 // ldmatrix moves pairs of 8-bit elements: a lane gets 4 neighbouring elements
 // of a token's keys, taken as elements 2t, 2t+1, 2t+8, 2t+9 of the product's
 // 16 (the queries are loaded in the same order), and 2 neighbouring elements of
@@ -405,6 +409,7 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
   static constexpr int DP = DP_, TT = TT_, NT = NT_, ESZ = 1, PITCH = DP + 16;
   static constexpr int kDtype = FWPKM_E4M3;
   static constexpr float kShift = 8.f;
+  unsigned lo[TT / 16][NT][2];
 
   __device__ __forceinline__ static int row_elem(int r) { return (r & 7) * 2 + (r >> 3); }
   __device__ __forceinline__ void load_q(const char *qp, int rows, int dim, float f) {
@@ -479,8 +484,12 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
 #pragma unroll
       for (int h = 0; h < NT; ++h)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          this->hi[n][h][i] = transpose8(pack_f16(s[n][h][2 * i], s[n][h][2 * i + 1]));
+        for (int i = 0; i < 2; ++i) {
+          const float x = s[n][h][2 * i], y = s[n][h][2 * i + 1];
+          const __half2 w = __floats2half2_rn(x, y);
+          this->hi[n][h][i] = transpose8(*reinterpret_cast<const unsigned *>(&w));
+          lo[n][h][i] = transpose8(pack_f16(x - __low2float(w), y - __high2float(w)));
+        }
   }
   __device__ __forceinline__ void outputs(const char *vs) {
     const int lane = threadIdx.x & 31;
@@ -498,8 +507,10 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
           e4m3_f16(__byte_perm(b[2 * j], 0, 0x3120), a[0], a[1]);
           e4m3_f16(__byte_perm(b[2 * j + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
-          for (int h = 0; h < NT; ++h)
+          for (int h = 0; h < NT; ++h) {
             mma_f16(this->o[2 * n + j][h], a, this->hi[k][h][0], this->hi[k][h][1]);
+            mma_f16(this->o[2 * n + j][h], a, lo[k][h][0], lo[k][h][1]);
+          }
         }
       }
   }

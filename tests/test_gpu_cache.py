@@ -429,6 +429,37 @@ def test_attend_equal_bits_and_streams():
         assert torch.equal(out, cache.attend(q, table, lens))
 
 
+def test_attend_e4m3_weights():
+    """8-bit caches: weights in the products with the values are as good as their sum.
+    Few tokens of opposite values leave outputs far smaller than their terms,
+    whose weights' rounding then shows."""
+    from sparse_weight_memory_b200 import KVCache
+    g = gen(35)
+    B, page, kv, heads, dim = 600, 16, 1, 8, 64
+    keys = torch.zeros((B, kv, page, dim), device="cuda")
+    keys[..., 0] = torch.randn((B, kv, page), generator=g, device="cuda").clamp(-2, 2)
+    values = torch.randn((B, kv, page, dim), generator=g, device="cuda")
+    cache = KVCache(keys=keys.to(E4), values=values.to(E4))
+    q = torch.zeros((B, heads, dim), device="cuda")
+    q[..., 0] = torch.rand((B, heads), generator=g, device="cuda") + 0.1
+    q = q.to(BF)
+    n = torch.arange(B, device="cuda", dtype=torch.int32) % 3 + 2
+    table = torch.arange(B, device="cuda", dtype=torch.int32)[:, None]
+    out = cache.attend(q, table, n, scale=0.5)
+    s = 0.5 * q.double()[:, :, :1] * cache.keys.double()[:, 0, None, :, 0]
+    s = s.masked_fill(torch.arange(page, device="cuda") >= n[:, None, None], -math.inf)
+    p, v = torch.softmax(s, -1), cache.values.double()[:, 0]
+    want, size = p @ v, p @ v.abs()
+    # half a step of the output; a score is one product, |s| <= 1.1, and its factor off
+    # by 2^-22; the exponent of up to 16 is rounded once, 2^-21; exp2 2^-22; these
+    # three twice; the two parts of a weight 2^-22; the sums of up to 4 terms,
+    # their join and the last factor 8 roundings
+    share = 2 * (2.0 ** -22 + 2.0 ** -21 + 2.0 ** -22) + 2.0 ** -22 + 8 * 2.0 ** -23
+    off = (out.double() - want).abs()
+    tol = 2.0 ** -8 * want.abs() + share * size
+    assert (off <= tol).all(), f"off by {(off / tol).max():.2f} of the tolerance"
+
+
 # -- append ---------------------------------------------------------------------
 
 def rotated(x, pos, freqs, style):
