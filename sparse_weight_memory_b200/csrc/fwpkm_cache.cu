@@ -177,7 +177,10 @@ extern "C" fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache,
 // tokens and alike: bf16 heads of 128 on 8, 10, 12 and 16 warps 192, 191, 185 and
 // 192 us, e4m3 143, 151, 150 and 157, bf16 heads of 64 147, 147, 142 and 142.
 // More than 8 query heads to a cached one are one segment of 16 or 32, since every
-// further segment reads the cached head again.
+// further segment reads the cached head again, unless that spills so much that two
+// segments take less: 32 heads to a cached e4m3 one of 128 (0.78 GB) 735 us as one
+// segment, 335 as two, 16 to one of 256 (0.83 GB) 600 and 283; 32 to one of 64
+// (0.39 GB) 196 as one and 224 as two.
 fwpkm::AttendShape fwpkm::attend_shape(int cache_dtype, int dim, int group) {
   const int dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
   if (cache_dtype == FWPKM_F32) {
@@ -185,9 +188,11 @@ fwpkm::AttendShape fwpkm::attend_shape(int cache_dtype, int dim, int group) {
     const int warps = heads == 16 || dp == 256 ? 8 : dp == 64 ? 16 : 12;
     return {warps, heads, heads * dp};
   }
-  const int heads = group <= 8 ? 8 : group <= 16 || dp == 256 ? 16 : 32;
+  const bool e4m3 = cache_dtype == FWPKM_E4M3;
+  const int most = !e4m3 ? (dp == 256 ? 16 : 32) : dp == 64 ? 32 : dp == 128 ? 16 : 8;
+  const int heads = group <= 8 || most == 8 ? 8 : group <= 16 || most == 16 ? 16 : 32;
   int warps = 16;
-  if (dp * heads >= 128 * 16 || (dp == 128 && cache_dtype == FWPKM_E4M3)) warps = 8;
+  if (dp * heads >= 128 * 16 || (dp == 128 && e4m3)) warps = 8;
   else if (dp == 128 || heads > 8) warps = 12;
   return {warps, heads, heads * dp};
 }

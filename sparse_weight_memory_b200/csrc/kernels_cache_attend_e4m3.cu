@@ -13,11 +13,9 @@ cudaError_t launch_cache_attend_e4m3(const AttendArgs &a, cudaStream_t st) {
            : s.heads == 16 ? launch<E4m3<64, 32, 2>, 12, 6>(a, st)
                            : launch<E4m3<64, 32, 4>, 8, 6>(a, st);
   if (a.p.dim <= 128)
-    return s.heads == 8    ? launch<E4m3<128, 32, 1>, 8, 6>(a, st)
-           : s.heads == 16 ? launch<E4m3<128, 32, 2>, 8, 5>(a, st)
-                           : launch<E4m3<128, 32, 4>, 8, 4>(a, st);
-  return s.heads == 8 ? launch<E4m3<256, 16, 1>, 8, 6>(a, st)
-                      : launch<E4m3<256, 16, 2>, 8, 4>(a, st);
+    return s.heads == 8 ? launch<E4m3<128, 32, 1>, 8, 6>(a, st)
+                        : launch<E4m3<128, 32, 2>, 8, 5>(a, st);
+  return launch<E4m3<256, 16, 1>, 8, 6>(a, st);
 }
 
 }  // namespace fwpkm
