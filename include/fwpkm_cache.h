@@ -57,7 +57,8 @@ enum {
  *   dtype     FWPKM_F32, FWPKM_BF16 or FWPKM_E4M3
  *   key_scale, value_scale   device fp32 [kv_heads] or NULL (1): an E4M3
  *             element e of head h stands for e * scale[h].  NULL for the
- *             other types.
+ *             other types.  A key scale that is not finite makes the scores of
+ *             its head's visible tokens NaN.
  */
 typedef struct {
   void *keys, *values;

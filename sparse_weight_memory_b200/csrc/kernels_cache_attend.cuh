@@ -439,8 +439,9 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
       // are normal numbers (a row of zeros, or one with infinities: 1)
       int e = (int)((__float_as_uint(top) >> 23) & 255u);
       e = e == 0 || e == 255 ? 127 : e < 2 ? 2 : e > 252 ? 252 : e;
+      // (f - f: a head whose scale is no number has no score that is one)
       const float down =
-          __uint_as_float(((unsigned)(254 - e) << 23) | (f < 0.f ? 0x80000000u : 0u));
+          __uint_as_float(((unsigned)(254 - e) << 23) | (f < 0.f ? 0x80000000u : 0u)) + (f - f);
       const float up = __uint_as_float((unsigned)e << 23);
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k) {

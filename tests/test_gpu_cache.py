@@ -460,6 +460,36 @@ def test_attend_e4m3_weights():
     assert (off <= tol).all(), f"off by {(off / tol).max():.2f} of the tolerance"
 
 
+@pytest.mark.parametrize("which", ["key_scale", "value_scale"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attend_bad_scale(which, bad):
+    """A cached head whose scale is no number gives no number for its query heads, in
+    sequences that are finished by a warp, joined in a CTA and joined across them,
+    and leaves the other heads their bits; a sequence without tokens has nothing
+    to scale."""
+    from sparse_weight_memory_b200 import KVCache
+    g = gen(31)
+    lengths = [9000, 1, 0, 700, 40]
+    table, pages = make_table(g, lengths, 32)
+    cache = make_pool(g, pages, 2, 32, 64, E4)
+    q = torch.randn((5, 6, 64), generator=g, device="cuda").to(BF)
+    scales = {"key_scale": cache._scales[0], "value_scale": cache._scales[1]}
+    scales[which] = scales[which].clone()
+    scales[which][1] = bad
+    broken = KVCache(keys=cache.keys, values=cache.values, **scales)
+    lse, want_lse = (torch.empty((5, 6), device="cuda") for _ in range(2))
+    want = cache.attend(q, table, as_int32(lengths), lse=want_lse)
+    out = broken.attend(q, table, as_int32(lengths), lse=lse)
+    live = [0, 1, 3, 4]
+    assert torch.equal(out[:, :3], want[:, :3]) and torch.equal(lse[:, :3], want_lse[:, :3])
+    assert not out[live, 3:].isfinite().any()
+    assert (out[2] == 0).all() and (lse[2] == -math.inf).all()
+    if which == "key_scale":
+        assert out[live, 3:].isnan().all() and lse[live, 3:].isnan().all()
+    else:
+        assert torch.equal(lse, want_lse)
+
+
 # -- append ---------------------------------------------------------------------
 
 def rotated(x, pos, freqs, style):
