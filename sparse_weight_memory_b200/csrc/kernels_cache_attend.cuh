@@ -43,7 +43,9 @@ namespace attend {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kLeastFactor = 1.18e-38f;  // a factor that no score feels, but not 0
+// In place of a factor 0, which would make a masked score (-infinity) no number: the
+// least number above it, which no score of 32 bits feels.
+constexpr float kLeastFactor = __FLT_DENORM_MIN__;
 // Warps of a CTA that take pieces, at the least (where it has so many): the
 // sums of those join in shared memory.  (One sequence of 1024 tokens: 12.6 us
 // with 1 to 8, 16.6 with 12.)

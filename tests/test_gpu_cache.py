@@ -490,6 +490,21 @@ def test_attend_bad_scale(which, bad):
         assert torch.equal(lse, want_lse)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [2e-38, -2e-39, 1e-41])
+def test_attend_tiny_scale(dtype, scale):
+    """Scales below the smallest normal number, with products large enough to feel them."""
+    from sparse_weight_memory_b200 import KVCache
+    g = gen(32)
+    keys = torch.zeros((4, 1, 16, 64), device="cuda")
+    keys[..., 0] = 2e19 * torch.rand((4, 1, 16), generator=g, device="cuda")
+    values = torch.randn((4, 1, 16, 64), generator=g, device="cuda")
+    cache = KVCache(keys=keys.to(dtype), values=values.to(dtype))
+    q = torch.zeros((1, 2, 64), device="cuda", dtype=dtype)
+    q[:, :, 0] = 8e18
+    check(cache, q, as_int32([[0, 1, 2, 3]]), [64], scale=scale)
+
+
 # -- append ---------------------------------------------------------------------
 
 def rotated(x, pos, freqs, style):
