@@ -438,9 +438,10 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
       top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
       top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
       // 2^-e and 2^e, e the exponent of the largest element kept where both
-      // are normal numbers (a row of zeros, or one with infinities: 1)
+      // are normal numbers (rows of denormal numbers then have elements under
+      // 1/2; beside an infinity the others do not matter, but stay finite)
       int e = (int)((__float_as_uint(top) >> 23) & 255u);
-      e = e == 0 || e == 255 ? 127 : e < 2 ? 2 : e > 252 ? 252 : e;
+      e = e < 2 ? 2 : e > 252 ? 252 : e;
       // (f - f: a head whose scale is no number has no score that is one)
       const float down =
           __uint_as_float(((unsigned)(254 - e) << 23) | (f < 0.f ? 0x80000000u : 0u)) + (f - f);

@@ -505,6 +505,28 @@ def test_attend_tiny_scale(dtype, scale):
     check(cache, q, as_int32([[0, 1, 2, 3]]), [64], scale=scale)
 
 
+def test_attend_rows_without_a_normal_exponent():
+    """8-bit caches: rows of queries with an infinity, beside elements beyond the 16-bit
+    range, and rows of denormal numbers only."""
+    from sparse_weight_memory_b200 import KVCache
+    g = gen(33)
+    keys = torch.rand((4, 1, 16, 64), generator=g, device="cuda") + 0.5
+    values = torch.randn((4, 1, 16, 64), generator=g, device="cuda")
+    one = torch.full((1,), 0.5, device="cuda")
+    cache = KVCache(keys=keys.to(E4), values=values.to(E4), key_scale=one, value_scale=one)
+    table, lens = as_int32([[0, 1, 2, 3]] * 2), as_int32([64, 64])
+    q = torch.zeros((2, 2, 64), device="cuda")
+    q[:, :, 1] = 1e6
+    q[:, 1] = torch.randn(64, generator=g, device="cuda")
+    q[:, 0, 0] = -math.inf
+    lse = torch.empty((2, 2), device="cuda")
+    out = cache.attend(q.to(BF), table, lens, lse=lse)
+    assert (out[:, 0] == 0).all() and (lse[:, 0] == -math.inf).all()
+    check(cache, q.to(BF)[:, 1:].contiguous(), table, [64, 64])
+    q = torch.randn((2, 2, 64), generator=g, device="cuda") * 2.0 ** -128
+    check(cache, q.to(BF), table, [64, 64], scale=1e38)
+
+
 # -- append ---------------------------------------------------------------------
 
 def rotated(x, pos, freqs, style):
