@@ -50,8 +50,11 @@ constexpr float kLeastFactor = __FLT_DENORM_MIN__;
 // sums of those join in shared memory.  (One sequence of 1024 tokens: 12.6 us
 // with 1 to 8, 16.6 with 12.)
 constexpr int kLeastPerCta = 8;
-// A score may exceed the reference by this (base 2) before the sums are scaled
-// to a new one: weights stay under 2^(kShift + kSlack).
+// A tile's scores may bring weights this much (base 2) above the largest one at the
+// time of the reference before the sums are scaled to a new one: weights stay
+// under 2^(kShift + kSlack).  kShift is -kSlack where values may be as large as 32
+// bits hold, so that no weight is above 1 and no sum leaves their range that
+// would not with weights of the softmax.
 constexpr float kSlack = 6.f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const char *src, bool ok) {
@@ -186,8 +189,8 @@ struct Mma {
     else
       return make_uint2(q[k][h][0], q[k][h][1]);
   }
-  // s: products; on return weights, in the same places.  kShift: the largest
-  // weight is 2^kShift when the reference is new.
+  // s: products; on return weights, in the same places.  shift: the largest
+  // weight is 2^shift when the reference is new.
   __device__ __forceinline__ void weigh(float (&s)[TT / 16][NT][4], unsigned vis, float shift) {
     const int g = (threadIdx.x & 31) >> 2;
     if (vis != FULL) {
@@ -302,6 +305,7 @@ struct Bf16 : Mma<Bf16<DP_, TT_, NT_>, DP_, TT_, NT_> {
   using Out = __nv_bfloat16;
   static constexpr int DP = DP_, TT = TT_, NT = NT_, ESZ = 2, PITCH = DP * 2 + 16;
   static constexpr int kDtype = FWPKM_BF16;
+  static constexpr float kShift = -kSlack;
   unsigned lo[TT / 16][NT][2];
 
   // Head element of row r of an output tile's 16.
@@ -342,7 +346,7 @@ struct Bf16 : Mma<Bf16<DP_, TT_, NT_>, DP_, TT_, NT_> {
           mma_bf16(s[n][h], a, q.x, q.y);
         }
       }
-    this->weigh(s, vis, 0.f);
+    this->weigh(s, vis, kShift);
 #pragma unroll
     for (int n = 0; n < TT / 16; ++n)
 #pragma unroll
@@ -549,6 +553,7 @@ struct F32 {
   using Out = float;
   static constexpr int DP = DP_, TT = 8, HEADS = RR_, RR = RR_, ESZ = 4, PITCH = DP * 4;
   static constexpr int kDtype = FWPKM_F32;
+  static constexpr float kShift = -kSlack;
   static constexpr int LG = 64 / RR, V4 = DP / LG / 4;  // lanes of a group, pieces of a lane
   static constexpr int NS = 16 / LG;                    // scores of a lane: tokens of one head
   static constexpr int kParts = 2 * V4, kQuery = 0;
@@ -634,10 +639,10 @@ struct F32 {
       if (!((vis >> (token() + j)) & 1u)) x[j] = kNegInf;
       top = fmaxf(top, x[j]);
     }
-    if (__any_sync(FULL, fmaf(top, c, -m) > kSlack)) {
+    if (__any_sync(FULL, fmaf(top, c, -m) > kShift + kSlack)) {
 #pragma unroll
       for (int w = 4 / NS; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, w));
-      top = fmaxf(m, top * c);
+      top = fmaxf(m, fmaf(top, c, -kShift));
       const float f = ex2(m - (top == kNegInf ? 0.f : top));
       m = top;
       l *= f;

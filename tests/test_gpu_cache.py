@@ -527,6 +527,26 @@ def test_attend_rows_without_a_normal_exponent():
     check(cache, q.to(BF), table, [64, 64], scale=1e38)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("batch,length", [(1500, 64), (3, 2000)])
+def test_attend_large_values(dtype, batch, length):
+    """Values whose sum over the tokens is still within 32 bits: weights are at most 1,
+    also where scores rise by less than what scales the sums anew (here by a
+    factor 2^5.9)."""
+    from sparse_weight_memory_b200 import KVCache
+    page = 32
+    pages = -(-length // page)
+    keys = torch.zeros((pages, 2, page, 64), device="cuda")
+    keys[1:, ..., 0] = 4.09375
+    values = torch.full_like(keys, 2e38 / length)
+    values[..., 1::2] *= -1
+    cache = KVCache(keys=keys.to(dtype), values=values.to(dtype))
+    q = torch.zeros((batch, 2, 64), device="cuda", dtype=dtype)
+    q[:, :, 0] = 1
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(batch, 1)
+    check(cache, q, table, [length] * batch, scale=1.0)
+
+
 # -- append ---------------------------------------------------------------------
 
 def rotated(x, pos, freqs, style):
