@@ -287,7 +287,12 @@ struct Mma {
 #pragma unroll
     for (int h = 0; h < NT; ++h)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) inv[h][e] = l[h][e] == 0.f ? 0.f : vs / l[h][e];
+      for (int e = 0; e < 2; ++e) {
+        inv[h][e] = l[h][e] == 0.f ? 0.f : vs / l[h][e];
+        if (l[h][e] == 0.f)  // nothing was weighed: 0, whatever the values are
+#pragma unroll
+          for (int n = 0; n < DP / 16; ++n) o[n][h][e] = o[n][h][2 + e] = 0.f;
+      }
     static_cast<Self *>(this)->write(out, rows, dim, inv);
     if (lse)
       stats([&](int h, float mh, float lh) {
@@ -705,6 +710,9 @@ struct F32 {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float f = __shfl_sync(FULL, inv, h * (LG / 2), LG);
+      if (f == 0.f)  // nothing was weighed: 0, whatever the values are
+#pragma unroll
+        for (int i = 0; i < V4; ++i) o[h][i][0] = o[h][i][1] = Pair{0.f, 0.f};
       const int row = lane() / LG * 2 + h;
 #pragma unroll
       for (int i = 0; i < V4; ++i) {

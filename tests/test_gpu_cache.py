@@ -547,6 +547,26 @@ def test_attend_large_values(dtype, batch, length):
     check(cache, q, table, [length] * batch, scale=1.0)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_attend_without_weights(dtype, value):
+    """A head whose visible scores are all -infinity gives 0 whatever its values are."""
+    g = gen(34)
+    lengths = [9000, 1, 700, 40]
+    table, pages = make_table(g, lengths, 32)
+    cache = make_pool(g, pages, 2, 32, 64, dtype)
+    cache.keys[:, 1, :, 0] = -math.inf
+    cache.values[:, 1, :, 3] = value
+    q = torch.randn((4, 6, 64), generator=g, device="cuda").to(dtype)
+    q[:, :, 0] = 1
+    lse = torch.empty((4, 6), device="cuda")
+    for width in (2, table.shape[1]):  # short contexts are divided another way
+        n = [min(m, 32 * width) for m in lengths]
+        out = cache.attend(q, table[:, :width].contiguous(), as_int32(n), lse=lse)
+        assert (out[:, 3:] == 0).all() and (lse[:, 3:] == -math.inf).all()
+        assert out[:, :3].isfinite().all()
+
+
 # -- append ---------------------------------------------------------------------
 
 def rotated(x, pos, freqs, style):
