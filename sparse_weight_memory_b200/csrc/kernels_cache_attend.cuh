@@ -1091,6 +1091,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) k_attend(const __grid_constant_
   if (lane == 0) last_seg[warp] = open ? seg : -1;
   if (open) {
     ty.total();
+    __syncwarp();  // every lane has read its last tile from the ring
     float4 *mine = reinterpret_cast<float4 *>(ring) + lane;
 #pragma unroll
     for (int i = 0; i < TY::kParts; ++i) mine[i * 32] = ty.part(i);
