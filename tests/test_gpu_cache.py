@@ -767,6 +767,37 @@ def test_append_many_sequences():
     assert torch.equal(cache.keys[at], k) and torch.equal(cache.values[at], 2 * k)
 
 
+@pytest.mark.parametrize("style", ["halves", "pairs"])
+@pytest.mark.parametrize("rows", [3, 3000])
+def test_append_small_sines(style, rows):
+    """cos and sin as accurate as their size, also near multiples of pi: the fraction
+    of a turn is not cut to 32 bits before them."""
+    from sparse_weight_memory_b200 import KVCache
+    g = gen(36)
+    cache = KVCache(pages=1, page_size=2 ** 16, kv_heads=1, dim=64, dtype=F32)
+    lengths = as_int32([rows + 1000])
+    pos = torch.arange(1000, rows + 1000, device="cuda")
+    # near a multiple of half a turn, from 2^-20 to 2^-2 turns beside it, at 1001
+    turns = torch.arange(1, 33, device="cuda") / 2
+    turns = turns + torch.sign(torch.randn(32, generator=g, device="cuda")) * \
+        2.0 ** -(2 + 18 * torch.rand(32, generator=g, device="cuda"))
+    freqs = (2 * math.pi * turns.double() / 1001).float()
+    q = torch.zeros((rows, 1, 64), device="cuda")  # a pair (1, 0) becomes (cos, sin)
+    one, two = (slice(0, 32), slice(32, 64)) if style == "halves" else (slice(0, 64, 2), slice(1, 64, 2))
+    q[..., one] = 1
+    kv = torch.zeros((rows, 1, 64), device="cuda")
+    got = cache.append(kv, kv, as_int32([[0]]), lengths, starts=as_int32([0, rows]), q=q,
+                       freqs=freqs, style=style)[:, 0].double()
+    angle = pos[:, None].double() * freqs.double()
+    # the function 2^-23 and the last rounding 2^-24 of the result; the angle four
+    # roundings in 64 bits; what 32 bits lose of the correction
+    # of up to pi 2^-25: its second order, its factors and products 2^-45
+    far = 4 * angle * 2.0 ** -53 + 2.0 ** -45
+    for part, want in ((one, angle.cos()), (two, angle.sin())):
+        off = (got[:, part] - want).abs()
+        assert (off <= (2.0 ** -23 + 2.0 ** -24) * want.abs() + far).all(), (off / want.abs()).max().item()
+
+
 # -- together -------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", [BF, E4, F32])
