@@ -134,10 +134,17 @@ fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache, const fwpkm_cache_batc
  * reads cached head i / (heads / kv_heads).  A sequence without visible tokens
  * gives out = 0 and lse = -infinity, and so does a head whose visible scores are
  * all -infinity; a NaN or +infinity among a head's visible scores makes that
- * sequence's head NaN, and no other.  Scores, softmax and sums are held in 32
- * bits, out is rounded once.  What lies in the pool outside the visible tokens
- * does not matter, infinities and NaN included.  The result does not depend on
- * timing: equal calls give equal bits.
+ * sequence's head NaN, and no other.  A NaN or an infinity among the visible
+ * values leaves that element of the heads that weigh it not finite (an infinity
+ * may come out as NaN), and no other.  What lies in the pool outside the visible
+ * tokens does not matter, infinities and NaN included.
+ *   Scores, the softmax's maximum and sum, and the sums of values are held in 32
+ * bits; with 16- and 8-bit pools a weight goes into its products with the values
+ * as two parts of the tensor cores' 16-bit types, 16 bits of it for an
+ * FWPKM_BF16 pool and 22 for an FWPKM_E4M3 one, and FWPKM_E4M3 pools take the
+ * queries in 16-bit floats scaled by a power of two a row, exact but for elements
+ * under 2^-14 of the row's largest (off by less than 2^-25 of that).  out is
+ * rounded once.  The result does not depend on timing: equal calls give equal bits.
  *   heads     query heads, a multiple of kv_heads, <= 4096
  *   q         device [B][heads][dim], sequence b at element b*q_stride (a whole
  *             number of 16 bytes; 16-byte aligned); FWPKM_F32 for an F32 cache,

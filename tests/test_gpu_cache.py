@@ -567,6 +567,26 @@ def test_attend_without_weights(dtype, value):
         assert out[:, :3].isfinite().all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attend_infinite_value(dtype):
+    """An infinite visible value leaves its element not finite, and the others their bits."""
+    g = gen(40)
+    lengths = [9000, 1, 700, 40]
+    table, pages = make_table(g, lengths, 32)
+    cache = make_pool(g, pages, 2, 32, 64, dtype)
+    q = torch.randn((4, 6, 64), generator=g, device="cuda").to(dtype)
+    lens = as_int32(lengths)
+    lse, want_lse = (torch.empty((4, 6), device="cuda") for _ in range(2))
+    want = cache.attend(q, table, lens, lse=want_lse)
+    rest = torch.ones((4, 6, 64), dtype=torch.bool, device="cuda")
+    for b, t, h, e in ((0, 8000, 0, 5), (1, 0, 1, 63), (2, 3, 1, 0), (3, 39, 0, 17)):
+        cache.values[table[b, t // 32].long(), h, t % 32, e] = math.inf
+        rest[b, 3 * h:3 * h + 3, e] = False
+    out = cache.attend(q, table, lens, lse=lse)
+    assert not out[~rest].isfinite().any()
+    assert torch.equal(out[rest], want[rest]) and torch.equal(lse, want_lse)
+
+
 # -- append ---------------------------------------------------------------------
 
 def rotated(x, pos, freqs, style):
