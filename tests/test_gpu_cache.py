@@ -587,6 +587,48 @@ def test_attend_infinite_value(dtype):
     assert torch.equal(out[rest], want[rest]) and torch.equal(lse, want_lse)
 
 
+@pytest.mark.parametrize("dtype", [BF, E4, F32])
+def test_attend_more_sequences_than_threads_joined(dtype):
+    """Several sequences to a thread, and parts of long ones joined across CTAs."""
+    g = gen(38)
+    lengths = [1] * 700 + [0] * 1200 + [40] * 298 + [9000, 3]
+    table, pages = make_table(g, lengths, 32)
+    cache = make_pool(g, pages, 2, 32, 64, dtype)
+    q = torch.randn((len(lengths), 4, 64), generator=g, device="cuda").to(F32 if dtype == F32 else BF)
+    check(cache, q, table, lengths)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attend_infinite_score(dtype):
+    """A +infinity among a head's scores makes that sequence's head NaN and no other,
+    where a warp finishes it and where parts are joined in a CTA or across them."""
+    from sparse_weight_memory_b200 import KVCache
+    g = gen(39)
+    lengths = [9000, 33, 700, 1, 6000]
+    table, pages = make_table(g, lengths, 32)
+    cache = make_pool(g, pages, 2, 32, 64, dtype)
+    q = torch.randn((5, 8, 64), generator=g, device="cuda").to(dtype)
+    sign = torch.tensor([1, -1, 0] * 3, device="cuda")[:8]  # of each head's element 0
+    q[..., 0] = sign.to(dtype)
+    places = ((0, 4321, 0), (1, 32, 1), (2, 0, 0), (2, 699, 1), (3, 0, 1))
+    near = cache.keys.clone()  # with a score of no weight (-250) for the heads of sign -1
+    bad = torch.zeros((5, 8), dtype=torch.bool, device="cuda")
+    for b, t, h in places:
+        at = (table[b, t // 32].long(), h, t % 32, 0)
+        cache.keys[at], near[at] = math.inf, 2000
+        bad[b, 4 * h:4 * h + 4] = sign[4 * h:4 * h + 4] >= 0  # infinity, or 0 times infinity
+    lse = torch.empty((5, 8), device="cuda")
+    out = cache.attend(q, table, as_int32(lengths), lse=lse)
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    none = torch.zeros_like(bad)  # the only token's score is -infinity
+    none[3, 4:] = sign[4:] < 0
+    assert (out[none] == 0).all() and (lse[none] == -math.inf).all()
+    want, tol, wl, ltol = reference(KVCache(keys=near, values=cache.values), q, table, lengths, 1 / 8, 0)
+    rest = ~bad & ~none
+    assert ((out.double() - want).abs() <= tol + 1e-37)[rest].all()
+    assert ((lse.double() - wl).abs() <= ltol)[rest].all()
+
+
 # -- append ---------------------------------------------------------------------
 
 def rotated(x, pos, freqs, style):
@@ -883,3 +925,52 @@ def test_prompt_then_tokens_beside_the_memory(dtype):
             want, size = want / ks, size / ks
         close(got.to(dtype), want, size, dtype)
     mem.close()
+
+
+def test_captured_behind_two_streams():
+    """Calls captured where two streams meet wait for the work of both."""
+    g = gen(37)
+    B, heads, kv, dim, page = 5, 4, 2, 128, 16
+    lengths = [3000, 1, 64, 65, 900]
+    table, pages = make_table(g, lengths, page)
+    cache = make_pool(g, pages, kv, page, dim, BF)
+    lens = as_int32(lengths)
+    freqs = torch.rand(dim // 2, generator=g, device="cuda")
+    big = torch.randn((4096, 4096), generator=g, device="cuda")
+    src = [torch.randn((B, heads + 2 * kv, dim), generator=g, device="cuda").to(BF) for _ in range(3)]
+    fed, qkv, n = src[0].clone(), torch.empty_like(src[0]), lens.clone()
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x = big @ big  # long enough that a call that did not wait would show
+            n.copy_(lens + (x[0, 0] * 0).int())
+        qkv.copy_(fed)
+        main.wait_stream(side)
+        q, k, v = qkv.split([heads, kv, kv], 1)
+        q = cache.append(k, v, table, n, q=q, freqs=freqs)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            out = cache.attend(q, table, n)
+        y = big @ big
+        main.wait_stream(side)
+        return q, out + (y[0, 0] * 0).to(BF)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got_q, got = step()
+    for x in src[1:]:
+        fed.copy_(x)
+        n.fill_(1)
+        qkv.zero_()
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        q, k, v = x.split([heads, kv, kv], 1)
+        want_q = cache.append(k, v, table, lens, q=q, freqs=freqs)
+        assert torch.equal(got_q, want_q)
+        assert torch.equal(got, cache.attend(want_q, table, lens))
