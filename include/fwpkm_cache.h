@@ -13,9 +13,9 @@
  *                       joined
  *
  * Conventions are those of fwpkm.h: pointers to memory the CALLER owns, on
- * the current CUDA device; work enqueued asynchronously on `stream`; status
- * codes, with the message in fwpkm_last_error(); argument checks on the host
- * before anything is enqueued.  Neither call allocates, synchronises or keeps
+ * the current CUDA device (4-byte aligned where nothing else is said); work
+ * enqueued asynchronously on `stream`; status codes, with the message in
+ * fwpkm_last_error(); argument checks on the host before anything is enqueued.  Neither call allocates, synchronises or keeps
  * anything from one call for the next, so calls on different streams need no
  * order beyond that of their data, and both may be captured into CUDA graphs.
  */

@@ -23,6 +23,7 @@ fwpkm_status fail(fwpkm_status st, const char *fmt, ...) {
 
 int elem_size(int dtype) { return dtype == FWPKM_F32 ? 4 : dtype == FWPKM_BF16 ? 2 : 1; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 constexpr int64_t kMaxRows = 1ll << 22;   // B * heads
 constexpr int kMaxHeads = 4096, kMaxKvHeads = 1024;
@@ -64,6 +65,8 @@ fwpkm_status check_pool(const char *who, const fwpkm_cache *c, CachePool *p) {
   }
   if ((c->key_scale || c->value_scale) && c->dtype != FWPKM_E4M3)
     return fail(FWPKM_EINVAL, "%s: only an FWPKM_E4M3 cache has scales", who);
+  if (!aligned4(c->key_scale) || !aligned4(c->value_scale))
+    return fail(FWPKM_EINVAL, "%s: scales must be 4-byte aligned", who);
   p->keys = static_cast<char *>(c->keys);
   p->values = static_cast<char *>(c->values);
   p->page_stride = c->page_stride * es;
@@ -85,7 +88,7 @@ fwpkm_status check_batch(const char *who, const fwpkm_cache_batch *b, CacheBatch
   if (b->table_stride < 0 || b->table_stride > kMaxStride)
     return fail(FWPKM_ESHAPE, "%s: table_stride must be 0 .. 2^40", who);
   if (!b->table || !b->lengths) return fail(FWPKM_EINVAL, "%s: table or lengths is NULL", who);
-  if ((reinterpret_cast<uintptr_t>(b->table) | reinterpret_cast<uintptr_t>(b->lengths)) & 3)
+  if (!aligned4(b->table) || !aligned4(b->lengths))
     return fail(FWPKM_EINVAL, "%s: table and lengths must be 4-byte aligned", who);
   s->table = b->table;
   s->lengths = b->lengths;
@@ -133,6 +136,8 @@ extern "C" fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache,
   if (style != FWPKM_ROTATE_HALVES && style != FWPKM_ROTATE_PAIRS)
     return fail(FWPKM_EINVAL, "%s: style must be FWPKM_ROTATE_HALVES or FWPKM_ROTATE_PAIRS", who);
   if (rotary && !freqs) return fail(FWPKM_EINVAL, "%s: freqs is NULL", who);
+  if (!aligned4(starts) || !aligned4(freqs) || !aligned4(device_errors))
+    return fail(FWPKM_EINVAL, "%s: starts, freqs and device_errors must be 4-byte aligned", who);
   if ((q == nullptr) != (q_out == nullptr))
     return fail(FWPKM_EINVAL, "%s: q and q_out must both be given, or neither", who);
   if (q && (heads < 1 || heads > kMaxHeads))
@@ -255,6 +260,8 @@ extern "C" fwpkm_status fwpkm_cache_attend(const fwpkm_cache *cache,
   if (!out || !aligned16(out))
     return fail(FWPKM_EINVAL, "%s: out must be given and 16-byte aligned", who);
   if (out == q) return fail(FWPKM_EINVAL, "%s: out must not be q", who);
+  if (!aligned4(lse) || !aligned4(device_errors))
+    return fail(FWPKM_EINVAL, "%s: lse and device_errors must be 4-byte aligned", who);
   const float scale_log2 = scale * 1.4426950408889634f;  // scores in base 2
   if (!std::isfinite(scale_log2))
     return fail(FWPKM_EINVAL, "%s: scale must be finite, and times log2(e) too", who);

@@ -263,6 +263,20 @@ def test_attend_refusals(lib, kw, status):
     assert call(lib, lib.fwpkm_cache_attend, ATTEND, pool(), batch(), **kw) == status
 
 
+@pytest.mark.parametrize("fn,args,c,kw", [
+    ("append", APPEND, dict(), dict(starts=FAKE + 2)), ("append", APPEND, dict(), dict(freqs=FAKE + 1)),
+    ("append", APPEND, dict(), dict(errors=FAKE + 2)),
+    ("append", APPEND, dict(dtype=2, key_scale=FAKE + 2), dict()),
+    ("attend", ATTEND, dict(dtype=2, value_scale=FAKE + 1), dict()),
+    ("attend", ATTEND, dict(), dict(lse=FAKE + 2)), ("attend", ATTEND, dict(), dict(errors=FAKE + 3)),
+])
+def test_words_that_are_not_aligned(lib, fn, args, c, kw):
+    """The kernels read and write them as 32-bit words."""
+    call_ = getattr(lib, "fwpkm_cache_" + fn)
+    assert call(lib, call_, args, pool(**c), batch(), **kw) == FWPKM_EINVAL
+    assert "4-byte aligned" in lib.fwpkm_last_error().decode()
+
+
 def test_null_descriptors_and_large_batches(lib):
     assert call(lib, lib.fwpkm_cache_append, APPEND, None, batch()) == FWPKM_EINVAL
     assert call(lib, lib.fwpkm_cache_append, APPEND, pool(), None) == FWPKM_EINVAL
