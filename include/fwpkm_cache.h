@@ -74,10 +74,11 @@ typedef struct {
 /*
  * The sequences of a call.  Token t of sequence b is row t % page_size of
  * page table[b*table_stride + t / page_size].
- *   B         sequences, >= 1; B * heads <= 2^22
- *   table     device int32, table_width entries a row.  Entries that no
- *             token of the call needs are not looked at (a page given back
- *             may be -1).
+ *   B         sequences, 1 .. 2^22 (in attend, B * heads <= 2^22)
+ *   table     device int32, table_width entries a row; rows may overlap
+ *             (table_stride >= 0, 0: one row for all), and sequences may share
+ *             pages that they do not write.  Entries that no token of the call
+ *             needs are not looked at (a page given back may be -1).
  *   lengths   device int32 [B]: tokens of sequence b, the new ones included.
  */
 typedef struct {

@@ -84,8 +84,9 @@ class KVCache:
     an 8-bit pool is multiplied by (default 1).
 
     Row b of ``table`` (int32 [B][width]) lists the pages of sequence b in
-    order; ``lengths`` (int32 [B]) are the sequences' tokens, the new ones
-    included.  Both lie on the device, so a captured graph follows them.
+    order (rows may overlap or be one row expanded: sequences may share pages);
+    ``lengths`` (int32 [B]) are the sequences' tokens, the new ones included.
+    Both lie on the device, so a captured graph follows them.
 
     ``stream`` (a torch stream or a handle) is where a call runs, the current
     one by default.  Tensors that the caller gives back before it has run there
@@ -169,7 +170,7 @@ class KVCache:
         if B >= _INT or width >= _INT:
             raise FwpkmError(FWPKM_ESHAPE, "table's sizes must be under 2^31")
         rows, cols = table.stride()
-        if (cols != 1 and width > 1) or (rows < width and B > 1):
+        if cols != 1 and width > 1:
             raise FwpkmError(FWPKM_ESHAPE, "table rows must be contiguous")
         return _Batch(B, width, rows if B > 1 else width, table.data_ptr(), lengths.data_ptr())
 

@@ -403,3 +403,13 @@ def test_pool_layouts(lib):
     c = KVCache(keys=both[:, 0].transpose(1, 2), values=both[:, 1].transpose(1, 2))
     assert (c.pages, c.kv_heads, c.page_size, c.dim) == (4, 2, 16, 64)
     assert (c._c.page_stride, c._c.head_stride, c._c.row_stride) == (2 * 16 * 128, 64, 128)
+
+
+def test_tables_may_overlap(lib):
+    """Rows that overlap, and one row for all, as the library takes them: such tables pass
+    the binding's checks (and are refused for the cache's device)."""
+    row = torch.zeros(8, dtype=torch.int32)
+    for table in (row.expand(2, -1), row.unfold(0, 6, 2)):
+        with pytest.raises(FwpkmError, match="not on a CUDA device"):
+            cpu_cache().append(**cpu_args(table=table))
+    assert cpu_cache()._batch(row.expand(2, -1), torch.ones(2, dtype=torch.int32)).table_stride == 0

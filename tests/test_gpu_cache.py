@@ -974,3 +974,18 @@ def test_captured_behind_two_streams():
         want_q = cache.append(k, v, table, lens, q=q, freqs=freqs)
         assert torch.equal(got_q, want_q)
         assert torch.equal(got, cache.attend(want_q, table, lens))
+
+
+def test_tables_with_shared_rows():
+    """Sequences that share a table row (one prefix, or the same row for all)."""
+    g = gen(41)
+    table, pages = make_table(g, [700], 16)
+    cache = make_pool(g, pages, 2, 16, 64, BF)
+    q = torch.randn((6, 4, 64), generator=g, device="cuda").to(BF)
+    lens = as_int32([700, 1, 0, 512, 33, 700])
+    want = cache.attend(q, table.repeat(6, 1), lens)
+    assert torch.equal(cache.attend(q, table.expand(6, -1), lens), want)
+    flat = table[0]
+    windows = flat.unfold(0, 8, 4)[:6]  # overlapping rows
+    lens = as_int32([128, 100, 3, 0, 128, 64])
+    assert torch.equal(cache.attend(q, windows, lens), cache.attend(q, windows.contiguous(), lens))
