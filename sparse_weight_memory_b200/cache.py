@@ -12,7 +12,8 @@ from typing import Optional
 
 import torch
 
-from .fwpkm import FWPKM_BF16, FWPKM_EINVAL, FWPKM_ESHAPE, FWPKM_F32, FwpkmError, load_library
+from .fwpkm import (FWPKM_BF16, FWPKM_EINVAL, FWPKM_ESHAPE, FWPKM_EUNSUPPORTED, FWPKM_F32,
+                    FwpkmError, load_library)
 
 E4M3 = 2                       # FWPKM_E4M3
 ROTATE = {"halves": 0, "pairs": 1}
@@ -73,6 +74,11 @@ def _shape(ok: bool, message: str):
         raise FwpkmError(FWPKM_ESHAPE, message)
 
 
+def _refuse_gradients():
+    raise FwpkmError(FWPKM_EUNSUPPORTED, "no gradients pass through the cache: call it under "
+                     "torch.no_grad(), or detach its inputs")
+
+
 class KVCache:
     """A paged cache of keys and values, written by ``append`` and read by ``attend``.
 
@@ -91,7 +97,9 @@ class KVCache:
     ``stream`` (a torch stream or a handle) is where a call runs, the current
     one by default.  Tensors that the caller gives back before it has run there
     need ``record_stream``, as for any work on a second stream.  No gradients
-    pass through either call.
+    pass through either call, so neither takes a tensor that requires them
+    while gradients are recorded (``torch.no_grad()`` or ``detach()`` says that
+    none are wanted).
     """
 
     def __init__(self, pages: Optional[int] = None, page_size: Optional[int] = None,
@@ -241,6 +249,10 @@ class KVCache:
             raise TypeError(f"unsupported dtype {dtype}")
         if style not in ROTATE:
             raise FwpkmError(FWPKM_EINVAL, f"style must be one of {sorted(ROTATE)}")
+        if torch.is_grad_enabled() and (
+                k.requires_grad or v.requires_grad or (q is not None and q.requires_grad) or
+                (freqs is not None and freqs.requires_grad)):
+            _refuse_gradients()
         rows = k.shape[0] if k.dim() else 0
         k_stride = self._rows(k, "k", dtype, rows, self.kv_heads)
         v_stride = self._rows(v, "v", dtype, rows, self.kv_heads)
@@ -295,6 +307,8 @@ class KVCache:
         dtype, B = q.dtype, batch.B
         if dtype not in _INPUTS:
             raise TypeError(f"unsupported dtype {dtype}")
+        if q.requires_grad and torch.is_grad_enabled():
+            _refuse_gradients()
         q_stride = self._rows(q, "q", dtype, B)
         heads = q.shape[1]
         need = self.attend_workspace(B, heads)

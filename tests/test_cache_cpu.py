@@ -413,3 +413,19 @@ def test_tables_may_overlap(lib):
         with pytest.raises(FwpkmError, match="not on a CUDA device"):
             cpu_cache().append(**cpu_args(table=table))
     assert cpu_cache()._batch(row.expand(2, -1), torch.ones(2, dtype=torch.int32)).table_stride == 0
+
+
+@pytest.mark.parametrize("name", ["k", "v", "q", "freqs"])
+def test_binding_refuses_to_drop_gradients(lib, name):
+    """No gradients pass: an input that requires them is refused while they are recorded."""
+    a = cpu_args(freqs=torch.ones(32))
+    a[name] = a[name].clone().requires_grad_()
+    calls = [lambda: cpu_cache().append(**a)]
+    if name == "q":
+        calls.append(lambda: cpu_cache().attend(a["q"], a["table"], a["lengths"]))
+    for call_ in calls:
+        with pytest.raises(FwpkmError, match="no gradients") as e:
+            call_()
+        assert e.value.status == FWPKM_EUNSUPPORTED
+        with torch.no_grad(), pytest.raises(FwpkmError, match="not on a CUDA device"):
+            call_()
