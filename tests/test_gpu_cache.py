@@ -629,6 +629,45 @@ def test_attend_infinite_score(dtype):
     assert ((lse.double() - wl).abs() <= ltol)[rest].all()
 
 
+@pytest.mark.parametrize("dtype,batch,width", [(BF, 2 ** 22, 1), (F32, 2 ** 20 + 3, 1), (E4, 300001, 400)])
+def test_attend_largest_batches(dtype, batch, width):
+    """Up to 2^22 sequences of 0 to 3 tokens, whole segments to a CTA or divided."""
+    from sparse_weight_memory_b200 import KVCache
+    g = gen(43)
+    page, dim = 4, 16
+    keys, values = (torch.randn((batch, 1, page, dim), generator=g, device="cuda").to(dtype)
+                    for _ in range(2))
+    cache = KVCache(keys=keys, values=values)
+    q = torch.randn((batch, 1, dim), generator=g, device="cuda").to(F32 if dtype == F32 else BF)
+    lengths = torch.randint(0, 4, (batch,), generator=g, device="cuda", dtype=torch.int32)
+    order = torch.randperm(batch, generator=g, device="cuda").int()
+    table = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
+    table[:, 0] = order
+    lse = torch.empty((batch, 1), device="cuda")
+    out = cache.attend(q, table, lengths, lse=lse)
+    raw = (lambda x: x.view(torch.uint8)) if dtype == E4 else (lambda x: x)
+    k, v = (raw(x)[order.long(), 0].view(dtype).double() for x in (keys, values))
+    s = (k @ q.double().transpose(1, 2))[..., 0] / 4
+    size = (k.abs() @ q.double().abs().transpose(1, 2))[..., 0] / 4
+    seen = torch.arange(page, device="cuda") < lengths[:, None]
+    s = s.masked_fill(~seen, -math.inf)
+    p = torch.softmax(s, -1).nan_to_num(0.0)
+    want, terms = (p[:, None] @ v)[:, 0], (p[:, None] @ v.abs())[:, 0]
+    # as in `reference`, for at most 3 tokens
+    ds = size.masked_fill(~seen, 0.0).amax(-1) * (dim + 16) * 2.0 ** -23
+    if dtype == E4:
+        ds += q.double().abs().amax((1, 2)) * k.abs().sum(-1).amax(-1) / 4 * 2.0 ** -25
+    pw = {BF: 2.0 ** -16, E4: 2.0 ** -11, F32: 2.0 ** -22}[dtype]
+    share = 2 * (ds + 2.0 ** -22) + pw + 65 * 2.0 ** -23
+    u = 2.0 ** -24 if dtype == F32 else 2.0 ** -8
+    assert ((out[:, 0].double() - want).abs() <= u * want.abs() + share[:, None] * terms + 1e-37).all()
+    some = lengths > 0
+    ls = torch.logsumexp(s[some], -1)
+    tol = ds[some] + 2.0 ** -22 + 65 * 2.0 ** -23 + 2.0 ** -21 * (ls.abs() + s[some].amax(-1).abs() + 9)
+    assert ((lse[some, 0].double() - ls).abs() <= tol).all()
+    assert (lse[~some] == -math.inf).all() and (out[~some] == 0).all()
+
+
 # -- append ---------------------------------------------------------------------
 
 def rotated(x, pos, freqs, style):
@@ -989,3 +1028,80 @@ def test_tables_with_shared_rows():
     windows = flat.unfold(0, 8, 4)[:6]  # overlapping rows
     lens = as_int32([128, 100, 3, 0, 128, 64])
     assert torch.equal(cache.attend(q, windows, lens), cache.attend(q, windows.contiguous(), lens))
+
+
+def test_two_layers_and_the_memory_between_them():
+    """A token through an attention layer, a memory step that reads and writes, and a second
+    attention layer, each call's output the next one's input with no other kernel
+    between them, captured and replayed: every bit as call by call with a
+    synchronisation after each."""
+    from sparse_weight_memory_b200 import FwPKMState
+    g = gen(42)
+    B, heads, kv, dim, page, steps = 3, 4, 2, 64, 8, 6
+    start = [700, 1, 40]
+    table, pages = make_table(g, [n + steps for n in start], page)
+    width = heads + 2 * kv
+    freqs = torch.rand(dim // 2, generator=g, device="cuda")
+    subkeys = torch.randn((1, 2, 32, heads * dim // 2), generator=g, device="cuda")
+    rows = torch.randn((1024, width * dim), generator=g, device="cuda")
+    gate = torch.full((B, 1), 0.7, device="cuda")
+    target = torch.randn((B, 1, width * dim), generator=g, device="cuda")
+    fed = [torch.randn((B, width, dim), generator=g, device="cuda").to(BF) for _ in range(steps)]
+    pools = [torch.randn((2, pages, kv, page, dim), generator=g, device="cuda").to(BF) for _ in range(2)]
+
+    class Model:
+        def __init__(self):
+            from sparse_weight_memory_b200 import KVCache
+            self.caches = [KVCache(keys=p[0].clone(), values=p[1].clone()) for p in pools]
+            self.mem = FwPKMState(1024, heads * dim, width * dim, 4, 1)
+            self.mem.set_graphs(False)
+            self.x = torch.empty((B, width, dim), dtype=BF, device="cuda")
+            self.lengths = as_int32(start)
+            self.inner = torch.empty((B, 1, width * dim), device="cuda")
+            self.reset()
+
+        def reset(self):
+            self.mem.set_tables(subkeys, rows)
+            for c, p in zip(self.caches, pools):
+                c.keys.copy_(p[0])
+                c.values.copy_(p[1])
+            self.lengths.copy_(as_int32(start))
+
+        def token(self, done=lambda: None):
+            self.lengths.add_(1)
+            q, k, v = self.x.split([heads, kv, kv], 1)
+            q = self.caches[0].append(k, v, table, self.lengths, q=q, freqs=freqs)
+            done()
+            out = self.caches[0].attend(q, table, self.lengths)
+            done()
+            self.mem.step(out.view(B, 1, heads * dim), target, gate, 0.5, out=self.inner)
+            done()
+            q, k, v = self.inner.view(B, width, dim).split([heads, kv, kv], 1)  # fp32 into bf16
+            turned = self.caches[1].append(k, v, table, self.lengths, q=q, freqs=freqs)
+            done()
+            last = self.caches[1].attend(turned.to(BF), table, self.lengths)
+            done()
+            return out, self.inner, turned, last
+
+    a, b = Model(), Model()
+    a.x.copy_(fed[0])
+    a.token()  # scratch before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = a.token()
+    a.reset()
+    for x in fed:
+        a.x.copy_(x)
+        b.x.copy_(x)
+        graph.replay()
+        want = b.token(torch.cuda.synchronize)
+        assert all(t.isfinite().all() for t in want)
+        for i, j in zip(got, want):
+            assert torch.equal(i, j)
+    for c, d in zip(a.caches, b.caches):
+        assert torch.equal(c.keys, d.keys) and torch.equal(c.values, d.values)
+    for i, j in zip(a.mem.get_tables(), b.mem.get_tables()):
+        assert torch.equal(i, j)
+    a.mem.close()
+    b.mem.close()
