@@ -177,10 +177,11 @@ extern "C" fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache,
 }
 
 // More warps hide more latency, as long as the outputs and queries of a
-// segment's heads fit their registers; with spills the loop takes two to four
-// times as long (e4m3 heads of 256 on 12 warps 507 us, on 8 150).  Measured on 2 M
-// tokens and alike: bf16 heads of 128 on 8, 10, 12 and 16 warps 192, 191, 185 and
-// 192 us, e4m3 143, 151, 150 and 157, bf16 heads of 64 147, 147, 142 and 142.
+// segment's heads fit their registers.  One cached head for 8 query heads, in
+// sequences of up to 40435 tokens, rings as deep as the shared memory allows: bf16
+// heads of 128 (1.03 GB) on 8, 10, 12 and 16 warps 192, 192, 185 and 193 us; of 64
+// (0.78 GB) 148, 148, 143 and 142; e4m3 heads of 128 (0.78 GB) 143, 155, 151 and,
+// with spills, 428; of 256 (0.83 GB) on 8 155 and, with spills, on 12 521.
 // More than 8 query heads to a cached one are one segment of 16 or 32, since every
 // further segment reads the cached head again, unless that spills so much that two
 // segments take less: 32 heads to a cached e4m3 one of 128 (0.78 GB) 735 us as one

@@ -1347,10 +1347,14 @@ cudaError_t launch(AttendArgs a, cudaStream_t st) {
     return cudaErrorInvalidConfiguration;  // the workspace has another layout
   a.blocks = (a.group + TY::HEADS - 1) / TY::HEADS;
   // Where no segment can have more than four tiles for each of a CTA's warps, a CTA
-  // takes whole ones and the second kernel falls away: 64 tokens of 8 cached heads
-  // 10.5 us instead of 12.5, 256 ragged sequences of up to 704 85 instead of 90, one
-  // of 512 14.6 instead of 12.5 in a graph but 15.4 instead of 16.8 as a call.
-  // Beyond, one sequence of 2048 would take 29 instead of 12.6.
+  // takes whole ones and the second kernel falls away.  In a graph, whole and divided
+  // (bf16 heads of 128): 64 tokens of 8 cached heads 10.4 us and 12.4, 300 sequences
+  // of 64 tokens and one head 12.6 and 15.8, 256 ragged ones of up to 704 and 4 heads
+  // 53.6 and 54.9.  What it loses is where a few segments of that length meet idle
+  // CTAs, or somewhat more of them than CTAs: one sequence of 736 tokens 16.7 and
+  // 14.7, 148, 160 and 300 segments of it 20.8 and 21.9, 27.0 and 25.4, 35.0 and 34.9.
+  // As calls of their own, small ones gain the second launch's host time (one of 512:
+  // 15.4 and 16.8).  Beyond the limit, one sequence of 2048 would take 29 and 12.6.
   a.aligned = a.tokens / TY::TT + 2 <= 4 * WARPS;
   e = launch_k(true, k_attend<TY, WARPS, UNITS>, dim3(kAttendCtas), dim3(WARPS * 32),
                Layout<TY, WARPS, UNITS>::kSmem, st, a);
