@@ -98,9 +98,10 @@ typedef struct {
  * read into the cache nor written in q_out.
  *   Rotation by position p: elements (a, b) of a pair j, 0 <= j < rotary/2,
  * become (a cos x - b sin x, b cos x + a sin x), x = p * freqs[j] formed in 64
- * bits.  Keys are rotated, rounded once to the cache's type (E4M3: after the
- * division by the head's scale, saturating at +-448) and stored; values are
- * stored as they are; queries, where given, are rotated into q_out.
+ * bits.  Keys are rotated in 32 bits, rounded to the cache's type (E4M3: after
+ * the division by the head's scale, saturating at +-448) and stored; values are
+ * stored without the rotation, in the same way; queries, where given, are
+ * rotated into q_out.
  *   rows      rows of k, v, q and q_out (0: nothing to do)
  *   in_dtype  type of k, v, q and q_out: FWPKM_F32 or FWPKM_BF16 (FWPKM_F32
  *             with any cache, FWPKM_BF16 with any cache)
@@ -150,7 +151,8 @@ fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache, const fwpkm_cache_batc
  *   q         device [B][heads][dim], sequence b at element b*q_stride (a whole
  *             number of 16 bytes; 16-byte aligned); FWPKM_F32 for an F32 cache,
  *             FWPKM_BF16 for the others (FWPKM_EUNSUPPORTED otherwise)
- *   scale     finite, below 2e38 in size; usually 1/sqrt(dim)
+ *   scale     finite, below 2e38 in size; usually 1/sqrt(dim).  With 0, a
+ *             product that is -infinity still has no weight
  *   window    tokens visible before and including the newest, or 0: all
  *   out       device [B][heads][dim], q's type, 16-byte aligned; like lse, it
  *             overlaps no input (q least of all)

@@ -236,7 +236,8 @@ class KVCache:
         ``freqs`` (fp32 [rotary/2], radians per token): the first ``rotary``
         elements of keys and queries turn by position, ``style`` "halves" or
         "pairs".  Returns the rotated ``q`` [rows][heads][dim] (in ``q_out``,
-        which may be ``q``), or None without ``q``."""
+        which may be ``q``), or None without ``q``.  Rows of no token (behind
+        the last sequence's, or of an empty one) are not written there."""
         if stream is not None or self._elsewhere():
             with self._other(stream):
                 return self._append(k, v, table, lengths, starts, q, freqs, style, q_out, errors)
