@@ -100,6 +100,32 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const unsigned (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same into sums of their own.
+__device__ __forceinline__ void mma_bf16_new(float (&d)[4], const unsigned (&a)[4], unsigned b0,
+                                             unsigned b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], const unsigned (&a)[4], unsigned b0,
+                                            unsigned b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// c += a, rounded to nearest, two in one instruction.
+__device__ __forceinline__ void add4(float (&c)[4], const float (&a)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2)
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(c[i]), "+f"(c[i + 1])
+        : "f"(a[i]), "f"(a[i + 1]));
+}
 // 2^x for x <= 0 or about so; results under 2^-126 are 0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -154,6 +180,11 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 // What the two tensor-core types share.  Thread (g = lane/4, t = lane%4).  s
 // and p: tokens 16n + g (+ 8), heads 8h + 2t (+ 1), the accumulator layout of
 // mma.m16n8.  o: head elements as rows, heads as columns.
+// The tensor cores cut what a product's sum has beyond 32 bits, which over
+// thousands of tokens adds up in one direction (to 2^-25 of o a product): they sum
+// a tile, and an addition of its own, rounded to nearest, takes that into o.  It
+// costs 0.5 to 1% with 8 bf16 heads, 2 to 8% with 8 e4m3 ones (8 cached heads of 128,
+// 1.17 GB: 208 and 211 us; of 256, 0.83 GB: 156 and 166), up to 9% with 32.
 // QS: the queries lie in shared memory, in the order in which the products take
 // them, where the outputs need the registers.
 template <typename Self, int DP_, int TT_, int NT_>
@@ -371,17 +402,22 @@ struct Bf16 : Mma<Bf16<DP_, TT_, NT_>, DP_, TT_, NT_> {
     const int lane = threadIdx.x & 31;
     const uint32_t a0 = smem_u32(vs) + ((lane & 7) + (lane >> 4) * 8) * PITCH + ((lane >> 3) & 1) * 16;
 #pragma unroll
-    for (int k = 0; k < TT / 16; ++k)
+    for (int n = 0; n < DP / 16; ++n) {
+      float x[NT][4];  // the tile's sums
 #pragma unroll
-      for (int n = 0; n < DP / 16; ++n) {
+      for (int k = 0; k < TT / 16; ++k) {
         unsigned a[4];
         ldsm4t(a, a0 + k * 16 * PITCH + n * 32);
 #pragma unroll
         for (int h = 0; h < NT; ++h) {
-          mma_bf16(this->o[n][h], a, this->hi[k][h][0], this->hi[k][h][1]);
-          mma_bf16(this->o[n][h], a, lo[k][h][0], lo[k][h][1]);
+          if (k == 0) mma_bf16_new(x[h], a, lo[k][h][0], lo[k][h][1]);
+          else mma_bf16(x[h], a, lo[k][h][0], lo[k][h][1]);
+          mma_bf16(x[h], a, this->hi[k][h][0], this->hi[k][h][1]);
         }
       }
+#pragma unroll
+      for (int h = 0; h < NT; ++h) add4(this->o[n][h], x[h]);
+    }
   }
   // The finished rows: out + row * dim, for the block's first `rows` heads.
   __device__ __forceinline__ void write(Out *out, int rows, int dim, const float (&inv)[NT][2]) {
@@ -512,9 +548,10 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
     const int lane = threadIdx.x & 31;
     const uint32_t a0 = smem_u32(vs) + (lane & 15) * PITCH + (lane >> 4) * 16;
 #pragma unroll
-    for (int k = 0; k < TT / 16; ++k)
+    for (int n = 0; n < DP / 32; ++n) {
+      float x[2][NT][4];  // the tile's sums
 #pragma unroll
-      for (int n = 0; n < DP / 32; ++n) {
+      for (int k = 0; k < TT / 16; ++k) {
         unsigned b[4];  // tokens 0-7 and 8-15 of 8 pairs of elements, then of the next 8
         ldsm4t(b, a0 + k * 16 * PITCH + n * 32);
 #pragma unroll
@@ -525,11 +562,17 @@ struct E4m3 : Mma<E4m3<DP_, TT_, NT_>, DP_, TT_, NT_> {
           e4m3_f16(__byte_perm(b[2 * j + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
           for (int h = 0; h < NT; ++h) {
-            mma_f16(this->o[2 * n + j][h], a, this->hi[k][h][0], this->hi[k][h][1]);
-            mma_f16(this->o[2 * n + j][h], a, lo[k][h][0], lo[k][h][1]);
+            if (k == 0) mma_f16_new(x[j][h], a, lo[k][h][0], lo[k][h][1]);
+            else mma_f16(x[j][h], a, lo[k][h][0], lo[k][h][1]);
+            mma_f16(x[j][h], a, this->hi[k][h][0], this->hi[k][h][1]);
           }
         }
       }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int h = 0; h < NT; ++h) add4(this->o[2 * n + j][h], x[j][h]);
+    }
   }
   __device__ __forceinline__ void write(Out *out, int rows, int dim, const float (&inv)[NT][2]) {
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;

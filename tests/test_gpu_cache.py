@@ -668,6 +668,35 @@ def test_attend_largest_batches(dtype, batch, width):
     assert (lse[~some] == -math.inf).all() and (out[~some] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("dim,heads", [(64, 8), (128, 8), (128, 16), (256, 8)])
+def test_attend_long_sums(dtype, dim, heads):
+    """Sums over many tokens are rounded to nearest, not cut: tokens that come twice, with
+    values of both signs, leave nothing, and what a cut at each step takes away
+    would show.  Each sequence is about a warp's work."""
+    from sparse_weight_memory_b200 import KVCache
+    g = gen(44)
+    batch, n, page = 1500, 25600, 64
+    pages = n // page
+    keys = torch.randn((pages // 2, 1, page, dim), generator=g, device="cuda") / math.sqrt(dim)
+    values = torch.rand((pages // 2, 1, page, dim), generator=g, device="cuda") + 1
+    cache = KVCache(keys=torch.cat([keys, keys]).to(dtype), values=torch.cat([values, -values]).to(dtype))
+    q = torch.randn((batch, heads, dim), generator=g, device="cuda").to(BF)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(batch, -1)
+    out = cache.attend(q, table, torch.full((batch,), n, dtype=torch.int32, device="cuda"), scale=1.0)
+    k, v = (x.double().transpose(0, 1).reshape(n, dim)[:n // 2] for x in (cache.keys, cache.values))
+    for b in range(0, batch, 100):
+        p = torch.softmax(q[b:b + 100].double() @ k.t(), -1)  # of one half
+        half = (p @ v) / 2
+        # sums rise to `half` and fall again.  n/16 additions rounded to nearest, 2^-24
+        # each, add up at random: six times their deviation.  Beside them, all in
+        # 2^-24: 16 for the products' sums inside a tile (cut, up to four at a time),
+        # 8 for the factors of two joined parts, 8 for exp2 and 2 for the weights' parts
+        tol = (6 * math.sqrt(n / 16) / math.sqrt(3) + 34) * 2.0 ** -24 * half
+        off = out[b:b + 100].double().abs()
+        assert (off <= tol).all(), f"off by {(off / tol).max():.1f} of the tolerance"
+
+
 # -- append ---------------------------------------------------------------------
 
 def rotated(x, pos, freqs, style):
