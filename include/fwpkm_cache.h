@@ -15,9 +15,10 @@
  * Conventions are those of fwpkm.h: pointers to memory the CALLER owns, on
  * the current CUDA device (4-byte aligned where nothing else is said); work
  * enqueued asynchronously on `stream`; status codes, with the message in
- * fwpkm_last_error(); argument checks on the host before anything is enqueued.  Neither call allocates, synchronises or keeps
- * anything from one call for the next, so calls on different streams need no
- * order beyond that of their data, and both may be captured into CUDA graphs.
+ * fwpkm_last_error(); argument checks on the host before anything is enqueued.
+ * Neither call allocates, synchronises or keeps anything from one call for the
+ * next, so calls on different streams need no order beyond that of their data,
+ * and both may be captured into CUDA graphs.
  */
 #ifndef FWPKM_CACHE_H_
 #define FWPKM_CACHE_H_
@@ -141,7 +142,7 @@ fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache, const fwpkm_cache_batc
  * may come out as NaN), and no other.  What lies in the pool outside the visible
  * tokens does not matter, infinities and NaN included.
  *   Scores, the softmax's maximum and sum, and the sums of values are held in 32
- * bits; with 16- and 8-bit pools a weight goes into its products with the values
+ * bits, the last rounded to nearest once for every 8 to 32 tokens; with 16- and 8-bit pools a weight goes into its products with the values
  * as two parts of the tensor cores' 16-bit types, 16 bits of it for an
  * FWPKM_BF16 pool and 22 for an FWPKM_E4M3 one, and FWPKM_E4M3 pools take the
  * queries in 16-bit floats scaled by a power of two a row, exact but for elements

@@ -179,14 +179,14 @@ extern "C" fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache,
 // More warps hide more latency, as long as the outputs and queries of a
 // segment's heads fit their registers.  One cached head for 8 query heads, in
 // sequences of up to 40435 tokens, rings as deep as the shared memory allows: bf16
-// heads of 128 (1.03 GB) on 8, 10, 12 and 16 warps 192, 192, 185 and 193 us; of 64
-// (0.78 GB) 148, 148, 143 and 142; e4m3 heads of 128 (0.78 GB) 143, 155, 151 and,
-// with spills, 428; of 256 (0.83 GB) on 8 155 and, with spills, on 12 521.
+// heads of 128 (1.03 GB) on 8, 10, 12 and 16 warps 191, 191, 185 and 191 us; of 64
+// (0.78 GB) 148, 148, 144 and 142; e4m3 heads of 128 (0.78 GB) 145, 163, 150 and,
+// with spills, 438; of 256 (0.83 GB) on 8 166 and, with spills, on 12 533.
 // More than 8 query heads to a cached one are one segment of 16 or 32, since every
 // further segment reads the cached head again, unless that spills so much that two
-// segments take less: 32 heads to a cached e4m3 one of 128 (0.78 GB) 735 us as one
-// segment, 335 as two, 16 to one of 256 (0.83 GB) 600 and 283; 32 to one of 64
-// (0.39 GB) 196 as one and 224 as two.
+// segments take less: 32 heads to a cached e4m3 one of 128 (0.78 GB) 730 us as one
+// segment, 372 as two, 16 to one of 256 (0.83 GB) 640 and 312; 32 to one of 64
+// (0.39 GB) 202 as one and 217 as two.
 fwpkm::AttendShape fwpkm::attend_shape(int cache_dtype, int dim, int group) {
   const int dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
   if (cache_dtype == FWPKM_F32) {

@@ -25,13 +25,13 @@
 // next to each other, the rest by k_join through the workspace.
 //
 // Measured (B200, calls back to back, the cache larger than the L2): 131072
-// bf16 tokens x 8 cached heads of 128, 0.54 GB, 103 us, 5.2 TB/s, 79% of the
-// measured copy rate; 1.17 GB of e4m3 in 32 ragged sequences 243 us, 73%, at the
-// board's power limit (207 us, 86%, in runs too short to reach it); one cached fp32
+// bf16 tokens x 8 cached heads of 128, 0.54 GB, 101 us, 5.3 TB/s, 81% of the
+// measured copy rate; 1.17 GB of e4m3 in 32 ragged sequences 231 us, 77%, at the
+// board's power limit (211 us, 85%, in runs too short to reach it); one cached fp32
 // head of 256 in 1 M tokens, 2.15 GB, 340 us for 4 query heads, 96%, and 385 for 8,
-// 85%.  What is left
-// at the large sizes: SMs in GPCs with more SMs get less bandwidth each (equal
-// pieces end between 71 and 97 us), 3 us before the first load and 5 at the end.
+// 85%.  What is left at the large sizes: SMs in GPCs with more SMs get less bandwidth
+// each (equal pieces end between 71 and 97 us), 3 us before the first load and 5 at
+// the end.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -445,10 +445,8 @@ struct Bf16 : Mma<Bf16<DP_, TT_, NT_>, DP_, TT_, NT_> {
 // part alone, 11 bits, left errors of 2^-12 of the terms, which show where an
 // output is far smaller than they are.  With up to 8 heads to a cached one the
 // second product takes no time by itself (8 cached heads of 128 with 8 query heads
-// each, 1.17 GB: 205 us with one, 200 with two) but power: at the board's limit the
-// same takes 227 and 241.  Padded widths take 8% longer (80: 139 and 150 us, 0.49
-// GB); with 16 heads to a cached one it is 160 and 178 us (heads of 128, 0.78 GB) and
-// 101 and 112 (of 64, 0.39 GB).
+// each, 1.17 GB: 205 us with one, 200 with two) but power: at the board's limit up to
+// 6%.  Padded widths take 8% longer, 16 heads to a cached one 11%.
 // ldmatrix moves pairs of 8-bit elements: a lane gets 4 neighbouring elements
 // of a token's keys, taken as elements 2t, 2t+1, 2t+8, 2t+9 of the product's
 // 16 (the queries are loaded in the same order), and 2 neighbouring elements of
