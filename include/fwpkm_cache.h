@@ -142,12 +142,13 @@ fwpkm_status fwpkm_cache_append(const fwpkm_cache *cache, const fwpkm_cache_batc
  * may come out as NaN), and no other.  What lies in the pool outside the visible
  * tokens does not matter, infinities and NaN included.
  *   Scores, the softmax's maximum and sum, and the sums of values are held in 32
- * bits, the last rounded to nearest once for every 8 to 32 tokens; with 16- and 8-bit pools a weight goes into its products with the values
- * as two parts of the tensor cores' 16-bit types, 16 bits of it for an
- * FWPKM_BF16 pool and 22 for an FWPKM_E4M3 one, and FWPKM_E4M3 pools take the
- * queries in 16-bit floats scaled by a power of two a row, exact but for elements
- * under 2^-14 of the row's largest (off by less than 2^-25 of that).  out is
- * rounded once.  The result does not depend on timing: equal calls give equal bits.
+ * bits; the last are rounded to nearest, once for every 8 to 32 tokens.  With 16-
+ * and 8-bit pools a weight goes into its products with the values as two parts of
+ * the tensor cores' 16-bit types, 16 bits of it for an FWPKM_BF16 pool and 22 for
+ * an FWPKM_E4M3 one.  FWPKM_E4M3 pools take the queries in 16-bit floats scaled by
+ * a power of two a row, exact but for elements under 2^-14 of the row's largest
+ * (off by less than 2^-25 of that).  out is rounded once.  The result does not
+ * depend on timing: equal calls give equal bits.
  *   heads     query heads, a multiple of kv_heads, <= 4096
  *   q         device [B][heads][dim], sequence b at element b*q_stride (a whole
  *             number of 16 bytes; 16-byte aligned); FWPKM_F32 for an F32 cache,
